@@ -21,10 +21,11 @@ ATTN_ERR_DEVICE_CHECK = 4
 ATTN_ERR_TIMEOUT = 5
 STATUS_NAMES = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_CUDA",
                 4: "ATTN_ERR_DEVICE_CHECK", 5: "ATTN_ERR_TIMEOUT"}
-DEVICE_TIMEOUT, DEVICE_BAD_PAGE, DEVICE_BAD_SEQLEN = 1, 2, 4
+DEVICE_TIMEOUT, DEVICE_BAD_PAGE, DEVICE_BAD_SEQLEN, DEVICE_BAD_OFFSETS = 1, 2, 4, 8
 
 # Every function include/attn.h declares, with its ctypes signature.
 _p, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_l, _ip = ctypes.c_int64, ctypes.POINTER(ctypes.c_int)
 SIGNATURES = {
     "attn_fwd": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _f, _p]),
     "attn_fwd_pos": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _f, _i, _f, _f, _p, _f, _p]),
@@ -37,6 +38,15 @@ SIGNATURES = {
     "attn_decode_step_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "attn_decode_step": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _f, _p, _p, _p, _sz,
                               _p]),
+    "attn_packed_fwd_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "attn_packed_fwd": (_i, [_p, _p, _p, _l, _l, _l, _p, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p, _sz, _p]),
+    "attn_packed_bwd_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "attn_packed_bwd": (_i, [_p, _p, _p, _l, _l, _l, _p, _p, _p, _p, _p, _p, _l, _l, _l, _p, _i, _i, _i, _i, _i, _i,
+                             _i, _f, _p, _sz, _p]),
+    "attn_chunk_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "attn_chunk_paged": (_i, [_p, _p, _p, _l, _l, _l, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p,
+                              _p, _p, _sz, _p]),
+    "attn_rope_axes": (_i, [_p, _p, _p, _p, _l, _l, _l, _l, _p, _i, _i, _i, _i, _i, _ip, _i, _i, _i, _f, _f, _i, _p]),
     "attn_debug_drop_copy": (None, [_i]),
     "attn_get_device_status": (_i, [_p, ctypes.POINTER(ctypes.c_int)]),
     "attn_last_error": (ctypes.c_char_p, []),
@@ -285,6 +295,199 @@ def attn_decode_paged_noalloc(q, k_pages, v_pages, block_table, seq_lens, scale=
                                          _dev_tensor(lse, "lse", torch.float32) if lse is not None else None,
                                          _stream(stream)))
     return o, lse
+
+
+def _token_rows(t, name):
+    """A bf16 tensor [T, heads, D] whose tokens hold their heads one behind the other, any distance
+    apart (a view of a fused projection's output is one): its pointer and token stride."""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    T, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if T > 1 else H * D
+
+
+class _Launch:
+    """Makes the device of the call's tensors current and the given stream torch's stream, so that
+    what the call allocates belongs to the stream it runs on."""
+
+    def __init__(self, stream, first, *others):
+        for t in others:
+            if t is not None and t.device != first.device:
+                raise ValueError("tensors of one call must be on one device, got %s and %s" % (first.device, t.device))
+        if first.device.type != "cuda":
+            raise TypeError("q must be a CUDA tensor")
+        self.device, self.guards = first.device, []
+        if first.device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(first.device))
+        self.given = stream
+
+    def __enter__(self):
+        if self.given is not None:
+            s = self.given
+            if not isinstance(s, torch.cuda.Stream):
+                s = torch.cuda.ExternalStream(int(getattr(s, "cuda_stream", s)), device=self.device)
+            self.guards.append(torch.cuda.stream(s))
+        for g in self.guards:
+            g.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _check_packed_shapes(q, k, v, cu_seqlens):
+    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or v.shape != k.shape:
+        raise ValueError("q must be [T, Hq, D], k and v [T, Hkv, D]")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be [num_seqs + 1]")
+
+
+def _workspace(given, need, device):
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if given is None else given
+    return _dev_tensor(ws, "workspace", torch.uint8), ws.numel(), ws
+
+
+def packed_fwd_workspace_size(T, num_seqs, Hq, Hkv, D) -> int:
+    return int(lib.attn_packed_fwd_workspace_size(T, num_seqs, Hq, Hkv, D))
+
+
+def attn_packed_fwd(q, k, v, cu_seqlens, causal=False, window=0, scale=0.0, o=None, lse=None, want_lse=True,
+                    workspace=None, stream=None):
+    """Attention forward over packed sequences of different lengths. q [T,Hq,D], k/v [T,Hkv,D] bf16 CUDA
+    tensors (token rows may be views, e.g. of one projection's output); sequence s owns rows
+    [cu_seqlens[s], cu_seqlens[s+1]), cu_seqlens int32 [num_seqs+1] on the device. Returns (o [T,Hq,D]
+    bf16, lse [Hq,T] fp32 or None); rows outside every sequence are not written."""
+    _check_packed_shapes(q, k, v, cu_seqlens)
+    T, Hq, D = q.shape
+    Hkv, S = k.shape[1], cu_seqlens.numel() - 1
+    if o is not None and o.shape != q.shape or lse is not None and lse.shape != (Hq, T):
+        raise ValueError("o must be [T, Hq, D] and lse [Hq, T]")
+    with _Launch(stream, q, k, v, cu_seqlens, o, lse, workspace) as st:
+        if o is None:
+            o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+        (qp, qs), (kp, ks), (vp, vs) = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
+        ws, ws_bytes, _keep = _workspace(workspace, packed_fwd_workspace_size(T, S, Hq, Hkv, D), q.device)
+        _check(lib.attn_packed_fwd(qp, kp, vp, qs, ks, vs, _dev_tensor(cu_seqlens, "cu_seqlens", torch.int32), S, T, Hq,
+                                   Hkv, D, int(bool(causal)), int(window), float(scale),
+                                   _dev_tensor(o, "o", torch.bfloat16),
+                                   _dev_tensor(lse, "lse", torch.float32) if lse is not None else None, ws, ws_bytes,
+                                   st))
+    return o, lse
+
+
+def packed_bwd_workspace_size(T, num_seqs, Hq, D) -> int:
+    return int(lib.attn_packed_bwd_workspace_size(T, num_seqs, Hq, D))
+
+
+def attn_packed_bwd(q, k, v, o, lse, dout, cu_seqlens, causal=False, window=0, scale=0.0, dq=None, dk=None, dv=None,
+                    workspace=None, stream=None):
+    """Gradients of attn_packed_fwd. o, dout [T,Hq,D] bf16 contiguous, lse [Hq,T] fp32 (from attn_packed_fwd
+    with the same arguments). Returns (dq, dk, dv), bf16, shaped as q, k, v; given ones may be views with
+    token strides of their own. Rows outside every sequence are not written."""
+    _check_packed_shapes(q, k, v, cu_seqlens)
+    T, Hq, D = q.shape
+    Hkv, S = k.shape[1], cu_seqlens.numel() - 1
+    if o.shape != q.shape or dout.shape != q.shape or lse.shape != (Hq, T):
+        raise ValueError("o and dout must be [T, Hq, D] and lse [Hq, T]")
+    for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        if t is not None and t.shape != like.shape:
+            raise ValueError("%s has another shape than its input" % name)
+    with _Launch(stream, q, k, v, o, lse, dout, cu_seqlens, dq, dk, dv, workspace) as st:
+        dq, dk, dv = (torch.empty(like.shape, dtype=torch.bfloat16, device=q.device) if t is None else t
+                      for t, like in ((dq, q), (dk, k), (dv, v)))
+        rows = [_token_rows(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v"), (dq, "dq"), (dk, "dk"), (dv, "dv"))]
+        ptr, strides = [r[0] for r in rows], [r[1] for r in rows]
+        ws, ws_bytes, _keep = _workspace(workspace, packed_bwd_workspace_size(T, S, Hq, D), q.device)
+        _check(lib.attn_packed_bwd(*ptr[:3], *strides[:3], _dev_tensor(o, "o", torch.bfloat16),
+                                   _dev_tensor(lse, "lse", torch.float32), _dev_tensor(dout, "dout", torch.bfloat16),
+                                   *ptr[3:], *strides[3:], _dev_tensor(cu_seqlens, "cu_seqlens", torch.int32), S, T, Hq,
+                                   Hkv, D, int(bool(causal)), int(window), float(scale), ws, ws_bytes, st))
+    return dq, dk, dv
+
+
+def chunk_workspace_size(T, num_seqs, max_blocks_per_seq, page_size, Hq, Hkv, D) -> int:
+    return int(lib.attn_chunk_workspace_size(T, num_seqs, max_blocks_per_seq, page_size, Hq, Hkv, D))
+
+
+def attn_chunk_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, k_new=None, v_new=None, window=0,
+                     scale=0.0, o=None, lse=None, want_lse=True, workspace=None, stream=None):
+    """Serving step with its own number of new tokens for every sequence (prompt chunks, single tokens,
+    none): append k_new/v_new into their page slots, then attend causally over the cache.
+    q [T,Hq,D], k_new/v_new [T,Hkv,D] bf16 or None (already appended); k_pages/v_pages
+    [num_pages,Hkv,page_size,D] bf16 (updated in place); block_table [S,max_blocks], seq_lens [S] (new tokens
+    counted) and cu_seqlens [S+1] int32, all CUDA. Nothing is rotated. Returns (o [T,Hq,D] bf16, lse [T,Hq]
+    fp32 or None)."""
+    if q.dim() != 3 or k_pages.dim() != 4 or k_pages.shape[3] != q.shape[2] or v_pages.shape != k_pages.shape:
+        raise ValueError("q must be [T, Hq, D] and k_pages/v_pages [num_pages, Hkv, page_size, D]")
+    T, Hq, D = q.shape
+    num_pages, Hkv, page_size, _ = k_pages.shape
+    S = cu_seqlens.numel() - 1
+    if S < 1 or cu_seqlens.dim() != 1 or seq_lens.shape != (S,) or block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("block_table must be [num_seqs, max_blocks], seq_lens [num_seqs], cu_seqlens [num_seqs + 1]")
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    if k_new is not None and (k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape):
+        raise ValueError("k_new/v_new must be [T, Hkv, D]")
+    if o is not None and o.shape != q.shape or lse is not None and lse.shape != (T, Hq):
+        raise ValueError("o must be [T, Hq, D] and lse [T, Hq]")
+    max_blocks = block_table.shape[1]
+    with _Launch(stream, q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, k_new, v_new, o, lse, workspace) as st:
+        if o is None:
+            o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        qp, qs = _token_rows(q, "q")
+        (kn, ks), (vn, vs) = ((_token_rows(k_new, "k_new"), _token_rows(v_new, "v_new")) if k_new is not None
+                              else ((None, 0), (None, 0)))
+        need = chunk_workspace_size(T, S, max_blocks, page_size, Hq, Hkv, D)
+        ws, ws_bytes, _keep = _workspace(workspace, need, q.device)
+        _check(lib.attn_chunk_paged(qp, kn, vn, qs, ks, vs, _dev_tensor(k_pages, "k_pages", torch.bfloat16),
+                                    _dev_tensor(v_pages, "v_pages", torch.bfloat16),
+                                    _dev_tensor(block_table, "block_table", torch.int32),
+                                    _dev_tensor(seq_lens, "seq_lens", torch.int32),
+                                    _dev_tensor(cu_seqlens, "cu_seqlens", torch.int32), S, T, max_blocks, num_pages,
+                                    page_size, Hq, Hkv, D, int(window), float(scale),
+                                    _dev_tensor(o, "o", torch.bfloat16),
+                                    _dev_tensor(lse, "lse", torch.float32) if lse is not None else None, ws, ws_bytes,
+                                    st))
+    return o, lse
+
+
+def attn_rope_axes(q, k, positions, sections, interleave_axes=False, per_axis_freq=False, rope_half_split=False,
+                   rope_base=10000.0, rope_pos_scale=1.0, inverse=False, q_out=None, k_out=None, stream=None):
+    """Rotary positions with several axes. q [T,Hq,D] and k [T,Hk,D] (or None) bf16 CUDA tensors (token rows
+    may be views), positions int32 [axes,T] on the device, sections the number of pairs of each axis.
+    inverse=True turns back, which is the rotation's gradient. q_out=q, k_out=k rotates in place.
+    Returns (q_out, k_out)."""
+    if q.dim() != 3 or k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]):
+        raise ValueError("q must be [T, Hq, D] and k [T, Hk, D]")
+    T, Hq, D = q.shape
+    if positions.shape != (len(sections), T):
+        raise ValueError("positions must be [len(sections), T]")
+    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if t is not None and (like is None or t.shape != like.shape):
+            raise ValueError("%s has another shape than its input" % name)
+    with _Launch(stream, q, k, positions, q_out, k_out) as st:
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        if k_out is None and k is not None:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+        (qp, qs), (qo, qos) = _token_rows(q, "q"), _token_rows(q_out, "q_out")
+        (kp, ks), (ko, kos) = ((_token_rows(k, "k"), _token_rows(k_out, "k_out")) if k is not None
+                               else ((None, 0), (None, 0)))
+        sec = (ctypes.c_int * len(sections))(*(int(x) for x in sections))
+        _check(lib.attn_rope_axes(qp, qo, kp, ko, qs, qos, ks, kos, _dev_tensor(positions, "positions", torch.int32), T,
+                                  Hq, 0 if k is None else k.shape[1], D, len(sections), sec, int(bool(interleave_axes)),
+                                  int(bool(per_axis_freq)), int(bool(rope_half_split)), float(rope_base),
+                                  float(rope_pos_scale), int(bool(inverse)), st))
+    return q_out, k_out
 
 
 def debug_drop_copy(enable: bool) -> None:

@@ -20,7 +20,9 @@
 #include "bwd_sm100.cuh"
 #include "decode.cuh"
 #include "fwd_sm100.cuh"
+#include "packed_sm100.cuh"
 #include "rope.cuh"
+#include "rope_axes.cuh"
 
 #define ATTN_VERSION_STRING "exact_attention_161_b200 0.2.0 (sm_100a)"
 
@@ -76,6 +78,24 @@ attn_status make_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_
     const cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                     const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return ATTN_OK;
+}
+
+// A rank-3 bf16 map of token-major rows [d2 tokens][d1 heads][d0 (contiguous)], tokens `stride`
+// elements apart, box {64 columns, box1 heads, box2 tokens}, 128-byte swizzle, tokens out of bounds
+// read as zero.
+attn_status make_map_tokens(CUtensorMap* map, const void* base, uint64_t d0, uint64_t heads, uint64_t tokens,
+                            uint64_t stride, uint32_t box1, uint32_t box2) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable (no CUDA driver?)");
+    const cuuint64_t dims[3] = {d0, heads, tokens};
+    const cuuint64_t strides[2] = {d0 * 2, stride * 2};
+    const cuuint32_t box[3] = {64, box1, box2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
@@ -572,6 +592,216 @@ attn_status launch_bwd(const void* q, const void* k, const void* v, const void* 
     return ATTN_OK;
 }
 
+// ------------------------------------------------------------------ packed sequences
+// Launch configuration of a kernel that may start while the one before it on the stream still runs
+// (it waits for it on the device).
+cudaLaunchConfig_t dependent_launch(unsigned grid, int threads, int smem, cudaStream_t stream,
+                                    cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(grid);
+    lc.blockDim = dim3(static_cast<unsigned>(threads));
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    lc.stream = stream;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return lc;
+}
+
+struct PackedCall {
+    const void *q, *k, *v;        // k, v: packed rows, or the pages
+    const void *k_new, *v_new;    // paged: to be appended, or NULL
+    long long qs, ks, vs;         // token strides in elements (paged: of q, k_new, v_new)
+    const int32_t *cu, *seq_lens, *block_table;
+    int T, S, Hq, Hkv, causal, window, max_blocks, num_pages;
+    float scale;
+    void* o;
+    float* lse;
+    void* ws;
+};
+
+template <int D, bool kPaged>
+attn_status launch_packed(const PackedCall& c, cudaStream_t stream, int dev) {
+    using C = attn::FwdCfg<D>;
+    const int G = c.Hq / c.Hkv, TT = 128 / G;
+    const long long max_keys = kPaged ? static_cast<long long>(c.max_blocks) * attn::kPageSize : c.T;
+    const attn::PlanLayout L = attn::plan_layout(c.T, c.S, TT, max_keys, c.Hkv, D);
+    uint8_t* w = static_cast<uint8_t*>(c.ws);
+    attn::PlanParams pl{};
+    pl.cu = c.cu;
+    pl.seq_lens = c.seq_lens;
+    pl.header = reinterpret_cast<attn::PlanHeader*>(w + L.header);
+    pl.prefix = reinterpret_cast<int*>(w + L.prefix);
+    pl.items = reinterpret_cast<attn::PackedItem*>(w + L.items);
+    pl.split = reinterpret_cast<attn::SplitBlock*>(w + L.split);
+    pl.S = c.S;
+    pl.T = c.T;
+    pl.TT = TT;
+    pl.Hkv = c.Hkv;
+    pl.causal = c.causal;
+    pl.window = c.window;
+    pl.max_len = static_cast<int>(kPaged ? max_keys : 0);
+    attn::AppendParams ap{};
+    unsigned append_blocks = 0;
+    int sms = 148;
+    CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    if (kPaged && c.k_new != nullptr) {
+        ap.k_new = static_cast<const __nv_bfloat16*>(c.k_new);
+        ap.v_new = static_cast<const __nv_bfloat16*>(c.v_new);
+        ap.k_pages = static_cast<__nv_bfloat16*>(const_cast<void*>(c.k));
+        ap.v_pages = static_cast<__nv_bfloat16*>(const_cast<void*>(c.v));
+        ap.block_table = c.block_table;
+        ap.ks = c.ks;
+        ap.vs = c.vs;
+        ap.max_blocks = c.max_blocks;
+        ap.num_pages = c.num_pages;
+        const long long want = (static_cast<long long>(c.T) * c.Hkv + 31) / 32;
+        append_blocks = static_cast<unsigned>(want < 2LL * sms ? want : 2LL * sms);
+    }
+    attn::packed_plan_kernel<D, kPaged, false><<<1 + append_blocks, attn::kPlanThreads, 0, stream>>>(pl, ap);
+    CUDA_TRY(cudaGetLastError());
+
+    attn::PackedParams p{};
+    p.header = pl.header;
+    p.items = pl.items;
+    p.block_table = c.block_table;
+    p.o = static_cast<__nv_bfloat16*>(c.o);
+    p.lse = c.lse;
+    p.ws_ml = reinterpret_cast<float*>(w + L.ml);
+    p.ws_o = reinterpret_cast<float*>(w + L.o);
+    p.lse_t = kPaged ? c.Hq : 1;
+    p.lse_h = kPaged ? 1 : c.T;
+    p.Hq = c.Hq;
+    p.Hkv = c.Hkv;
+    p.G = G;
+    p.TT = TT;
+    p.causal = c.causal;
+    p.window = c.window;
+    p.max_blocks = c.max_blocks;
+    p.num_pages = c.num_pages;
+    p.scale_log2 = c.scale * attn::kLog2e;
+    p.debug_drop_copy = g_debug_drop_copy.load() ? 1 : 0;
+    CUtensorMap tq, tk, tv;
+    attn_status st;
+    if ((st = make_map_tokens(&tq, c.q, D, c.Hq, c.T, c.qs, G, TT)) != ATTN_OK) return st;
+    if (kPaged) {
+        const uint64_t slabs = static_cast<uint64_t>(c.num_pages) * c.Hkv;
+        if ((st = make_map_3d(&tk, c.k, D, attn::kPageSize, slabs, attn::kPageSize)) != ATTN_OK) return st;
+        if ((st = make_map_3d(&tv, c.v, D, attn::kPageSize, slabs, attn::kPageSize)) != ATTN_OK) return st;
+    } else {
+        if ((st = make_map_tokens(&tk, c.k, D, c.Hkv, c.T, c.ks, 1, 128)) != ATTN_OK) return st;
+        if ((st = make_map_tokens(&tv, c.v, D, c.Hkv, c.T, c.vs, 1, 128)) != ATTN_OK) return st;
+    }
+    const long long most = L.max_items * c.Hkv;  // the device knows how many there are
+    const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
+    if ((st = ensure_smem(attn::attn_packed_kernel<D, kPaged>, C::SMEM_BYTES, dev)) != ATTN_OK) return st;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t lc = dependent_launch(grid, C::THREADS, C::SMEM_BYTES, stream, attr);
+    CUDA_TRY(cudaLaunchKernelEx(&lc, attn::attn_packed_kernel<D, kPaged>, tq, tk, tv, p));
+    if (L.max_slots > 0) {
+        lc = dependent_launch(static_cast<unsigned>(2 * sms), 256, 0, stream, attr);
+        CUDA_TRY(cudaLaunchKernelEx(&lc, attn::packed_merge_kernel<D>, p,
+                                    static_cast<const attn::SplitBlock*>(pl.split)));
+    }
+    return ATTN_OK;
+}
+
+template <int D>
+attn_status launch_packed_bwd(const void* q, const void* k, const void* v, long long qs, long long ks, long long vs,
+                              const void* o, const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                              long long dqs, long long dks, long long dvs, const int32_t* cu, int S, int T, int Hq,
+                              int Hkv, int causal, int window, float scale, void* ws, cudaStream_t stream, int dev) {
+    using C = attn::BwdCfg<D>;
+    const attn::BwdPlanLayout L = attn::bwd_plan_layout(T, S, Hq, D);
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    attn::PlanParams pl{};
+    pl.cu = cu;
+    pl.header = reinterpret_cast<attn::PlanHeader*>(w + L.header);
+    pl.prefix = reinterpret_cast<int*>(w + L.prefix);
+    pl.tiles = reinterpret_cast<attn::PackedTile*>(w + L.tiles);
+    pl.order = reinterpret_cast<int*>(w + L.order);
+    pl.S = S;
+    pl.T = T;
+    pl.TT = 64;
+    pl.Hkv = Hkv;
+    pl.causal = causal;
+    pl.window = window;
+    attn::packed_plan_kernel<D, false, true><<<1, attn::kPlanThreads, 0, stream>>>(pl, attn::AppendParams{});
+    CUDA_TRY(cudaGetLastError());
+    attn::BwdParams p{};
+    p.o = static_cast<const __nv_bfloat16*>(o);
+    p.dout = static_cast<const __nv_bfloat16*>(dout);
+    p.lse = lse;
+    p.vec = reinterpret_cast<float*>(w + L.vec);
+    p.dq = static_cast<__nv_bfloat16*>(dq);
+    p.dqacc = reinterpret_cast<float*>(w + L.dqacc);
+    p.dk = static_cast<__nv_bfloat16*>(dk);
+    p.dv = static_cast<__nv_bfloat16*>(dv);
+    p.B = 1;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.causal = causal;
+    p.window = window;
+    p.scale = scale;
+    p.scale_log2 = scale * attn::kLog2e;
+    p.debug_drop_copy = g_debug_drop_copy.load() ? 1 : 0;
+    p.header = pl.header;
+    p.tiles = pl.tiles;
+    p.order = pl.order;
+    p.dq_stride = dqs;
+    p.dk_stride = dks;
+    p.dv_stride = dvs;
+    p.T = T;
+    int sms = 148;
+    CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    CUtensorMap tq, tk, tv, tdo, tdq;
+    attn_status st;
+    if ((st = make_map_tokens(&tq, q, D, Hq, T, qs, 1, 128)) != ATTN_OK) return st;
+    if ((st = make_map_tokens(&tk, k, D, Hkv, T, ks, 1, 128)) != ATTN_OK) return st;
+    if ((st = make_map_tokens(&tv, v, D, Hkv, T, vs, 1, 128)) != ATTN_OK) return st;
+    if ((st = make_map_tokens(&tdo, dout, D, Hq, T, static_cast<uint64_t>(Hq) * D, 1, 128)) != ATTN_OK) return st;
+    if ((st = make_map_2d_f32(&tdq, p.dqacc, D, static_cast<uint64_t>(L.max_tiles) * Hq * 128)) != ATTN_OK) return st;
+    if ((st = ensure_smem(attn::attn_bwd_kernel<D, true>, C::SMEM_BYTES, dev)) != ATTN_OK) return st;
+    cudaLaunchAttribute attr[1];
+    // rows a block of the prep pass and of the dq pass takes at a time
+    const long long rows = L.max_tiles * Hq * 128, prep = (rows * (D / 8) + 255) / 256;
+    const unsigned pass_grid = static_cast<unsigned>(prep < 16LL * sms ? prep : 16LL * sms);
+    cudaLaunchConfig_t lc = dependent_launch(pass_grid, 256, 0, stream, attr);
+    CUDA_TRY(cudaLaunchKernelEx(&lc, attn::bwd_prep_kernel<D, true>, static_cast<const attn::BwdParams>(p)));
+    lc = dependent_launch(static_cast<unsigned>(L.max_tiles * Hkv), C::THREADS, C::SMEM_BYTES, stream, attr);
+    CUDA_TRY(cudaLaunchKernelEx(&lc, attn::attn_bwd_kernel<D, true>, tq, tk, tv, tdo, tdq, p));
+    lc = dependent_launch(pass_grid, 256, 0, stream, attr);
+    CUDA_TRY(cudaLaunchKernelEx(&lc, attn::bwd_dq_store_packed_kernel<D>, static_cast<const attn::BwdParams>(p)));
+    return ATTN_OK;
+}
+
+// Checks shared by the entry points on packed sequences.
+attn_status check_packed(int T, int S, int Hq, int Hkv, int D, int causal, int window, float scale) {
+    if (T < 0 || S < 1 || Hq < 1 || Hkv < 1) return fail(ATTN_ERR_INVALID_ARG, "Hq, Hkv, num_seqs must be >= 1 and T >= 0");
+    if (Hq % Hkv != 0) return fail(ATTN_ERR_INVALID_ARG, "Hq (%d) must be a multiple of Hkv (%d)", Hq, Hkv);
+    if (causal != 0 && causal != 1) return fail(ATTN_ERR_INVALID_ARG, "causal must be 0 or 1");
+    if (window > 0 && !causal) return fail(ATTN_ERR_INVALID_ARG, "a sliding window requires causal = 1");
+    if (!std::isfinite(scale)) return fail(ATTN_ERR_INVALID_ARG, "scale must be finite");
+    if (D != 64 && D != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", D);
+    if (Hq / Hkv > 128) return fail(ATTN_ERR_UNSUPPORTED, "more than 128 query heads per KV head");
+    if (T >= (1 << 30) || S >= (1 << 24)) return fail(ATTN_ERR_UNSUPPORTED, "T must be < 2^30 and num_seqs < 2^24");
+    return ATTN_OK;
+}
+// A token-major [T, heads, D] tensor: 16-byte aligned rows that do not overlap.
+attn_status check_rows(const char* name, const void* ptr, long long stride, int heads, int D) {
+    if (!ptr) return fail(ATTN_ERR_INVALID_ARG, "%s must be non-NULL", name);
+    if (!aligned16(ptr)) return fail(ATTN_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+    if (stride < static_cast<long long>(heads) * D || stride % 8 != 0 || stride >= (1LL << 38))
+        return fail(ATTN_ERR_INVALID_ARG, "%s: token stride %lld must be a multiple of 8, >= heads * D and < 2^38", name, stride);
+    return ATTN_OK;
+}
+// Overflow limits of the device's 32-bit indices: items (blocks and parts for every K/V head), and
+// rows of packed tiles.
+bool too_many_rows(long long T, long long S, int heads) {
+    return static_cast<double>(T / 128 + (S < T ? S : T) + 1) * 128 * heads >= 2147483648.0;
+}
+
 // Forgets the cached device addresses of the no-alloc decode's array (defined with it below).
 void noalloc_forget();
 
@@ -795,6 +1025,260 @@ attn_status attn_decode_step(const void* q, const void* k_new, const void* v_new
                                  num_pages, Hq, Hkv, scale, o, lse, workspace, s, dev);
     return launch_decode<128>(q_use, k_pages, v_pages, block_table, seq_lens, num_seqs, q_len, max_blocks_per_seq,
                               num_pages, Hq, Hkv, scale, o, lse, workspace, s, dev);
+}
+
+attn_status attn_rope_axes(const void* q, void* q_out, const void* k, void* k_out, int64_t q_stride,
+                           int64_t q_out_stride, int64_t k_stride, int64_t k_out_stride, const int32_t* positions,
+                           int T, int Hq, int Hk, int D, int n_axes, const int* sections, int interleave_axes,
+                           int per_axis_freq, int rope_half_split, float rope_base, float rope_pos_scale, int inverse,
+                           void* stream) {
+    g_last_error.clear();
+    if (T < 0 || Hq < 1 || Hk < 0) return fail(ATTN_ERR_INVALID_ARG, "Hq must be >= 1, Hk and T >= 0");
+    if (!sections || n_axes < 1) return fail(ATTN_ERR_INVALID_ARG, "sections must name the pairs of at least one axis");
+    for (const int flag : {interleave_axes, per_axis_freq, rope_half_split, inverse})
+        if (flag != 0 && flag != 1)
+            return fail(ATTN_ERR_INVALID_ARG, "interleave_axes, per_axis_freq, rope_half_split and inverse must be 0 or 1");
+    if (!(std::isfinite(rope_base) && rope_base > 0.f) || !(std::isfinite(rope_pos_scale) && rope_pos_scale > 0.f))
+        return fail(ATTN_ERR_INVALID_ARG, "rope_base and rope_pos_scale must be finite and > 0");
+    if (D != 64 && D != 128) return fail(ATTN_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", D);
+    if (n_axes > attn::kRopeAxesMax) return fail(ATTN_ERR_UNSUPPORTED, "more than %d axes", attn::kRopeAxesMax);
+    if (T >= (1 << 30)) return fail(ATTN_ERR_UNSUPPORTED, "T must be < 2^30");
+    if (Hq > 32767 || Hk > 32767) return fail(ATTN_ERR_UNSUPPORTED, "more than 32767 heads");
+    long long pairs = 0;
+    for (int a = 0; a < n_axes; ++a) {
+        if (sections[a] < 1) return fail(ATTN_ERR_INVALID_ARG, "every axis needs at least one pair");
+        pairs += sections[a];
+    }
+    if (pairs > D / 2) return fail(ATTN_ERR_INVALID_ARG, "sections sum to %lld pairs, a head has %d", pairs, D / 2);
+    if (pairs % 8 != 0) return fail(ATTN_ERR_UNSUPPORTED, "the sections must sum to a multiple of 8 pairs");
+    attn::RopeAxesParams p{};
+    p.pairs = static_cast<int>(pairs);
+    int seen[attn::kRopeAxesMax] = {};
+    int at = 0, left = sections[0];
+    for (int i = 0; i < p.pairs; ++i) {
+        int a;
+        if (interleave_axes) {
+            a = i % n_axes;
+            if (i >= static_cast<long long>(n_axes) * sections[a]) a = 0;
+        } else {
+            while (left == 0) left = sections[++at];
+            a = at;
+            --left;
+        }
+        const double e = per_axis_freq ? static_cast<double>(seen[a]) / sections[a] : static_cast<double>(i) / p.pairs;
+        ++seen[a];
+        p.axis[i] = static_cast<uint8_t>(a);
+        p.rev[i] = std::pow(static_cast<double>(rope_base), -e) / (6.283185307179586476925 * rope_pos_scale);
+    }
+    for (int a = 0; a < n_axes; ++a)
+        if (seen[a] != sections[a])
+            return fail(ATTN_ERR_INVALID_ARG, "axis %d cannot take every %d-th of %lld pairs for its %d", a, n_axes, pairs,
+                        sections[a]);
+    if (T == 0) return ATTN_OK;
+    if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u))
+        return fail(ATTN_ERR_INVALID_ARG, "positions must be non-NULL and 4-byte aligned");
+    attn_status st;
+    if ((st = check_rows("q", q, q_stride, Hq, D)) != ATTN_OK) return st;
+    if ((st = check_rows("q_out", q_out, q_out_stride, Hq, D)) != ATTN_OK) return st;
+    if (Hk > 0) {
+        if ((st = check_rows("k", k, k_stride, Hk, D)) != ATTN_OK) return st;
+        if ((st = check_rows("k_out", k_out, k_out_stride, Hk, D)) != ATTN_OK) return st;
+    }
+    p.src[0] = static_cast<const __nv_bfloat16*>(q);
+    p.dst[0] = static_cast<__nv_bfloat16*>(q_out);
+    p.src[1] = static_cast<const __nv_bfloat16*>(k);
+    p.dst[1] = static_cast<__nv_bfloat16*>(k_out);
+    p.src_stride[0] = q_stride;
+    p.dst_stride[0] = q_out_stride;
+    p.src_stride[1] = k_stride;
+    p.dst_stride[1] = k_out_stride;
+    p.pos = positions;
+    p.heads[0] = Hq;
+    p.heads[1] = Hk;
+    p.T = T;
+    p.half = rope_half_split;
+    p.sign = inverse ? -1.f : 1.f;
+    int dev = 0, sms = 148;
+    CUDA_TRY(cudaGetDevice(&dev));
+    CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    // tokens a CTA rotates at a time: enough for four items per thread, but no fewer than two CTAs per
+    // SM while there are tokens for them
+    const int per_token = (Hq + Hk) * (D / 16);
+    int group = 1024 / per_token;
+    group = group < 1 ? 1 : group > 16 ? 16 : group;
+    while (group > 1 && T / group < 2 * sms) group /= 2;
+    p.group = group;
+    const long long want = (static_cast<long long>(T) + group - 1) / group;
+    const unsigned grid = static_cast<unsigned>(want < 8LL * sms ? want : 8LL * sms);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (D == 64)
+        attn::rope_axes_kernel<64><<<grid, 256, 0, s>>>(p);
+    else
+        attn::rope_axes_kernel<128><<<grid, 256, 0, s>>>(p);
+    CUDA_TRY(cudaGetLastError());
+    return ATTN_OK;
+}
+
+size_t attn_packed_fwd_workspace_size(int T, int num_seqs, int Hq, int Hkv, int D) {
+    if (T < 1 || num_seqs < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0 || Hq / Hkv > 128) return 0;
+    return attn::plan_layout(T, num_seqs, 128 / (Hq / Hkv), T, Hkv, D).total;
+}
+
+attn_status attn_packed_fwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, const int32_t* cu_seqlens, int num_seqs, int T, int Hq, int Hkv, int D,
+                            int causal, int window, float scale, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    g_last_error.clear();
+    attn_status st = check_packed(T, num_seqs, Hq, Hkv, D, causal, window, scale);
+    if (st != ATTN_OK) return st;
+    if (T == 0) return ATTN_OK;
+    if ((st = check_rows("q", q, q_stride, Hq, D)) != ATTN_OK) return st;
+    if ((st = check_rows("k", k, k_stride, Hkv, D)) != ATTN_OK) return st;
+    if ((st = check_rows("v", v, v_stride, Hkv, D)) != ATTN_OK) return st;
+    if (!o || !workspace || !cu_seqlens) return fail(ATTN_ERR_INVALID_ARG, "o, workspace and cu_seqlens must be non-NULL");
+    if (!aligned16(o) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return fail(ATTN_ERR_INVALID_ARG, "misaligned pointer (tensors 16-byte, int32/fp32 arrays 4-byte)");
+    if (too_many_rows(T, num_seqs, Hq)) return fail(ATTN_ERR_UNSUPPORTED, "too many rows: (T + 128 num_seqs) * Hq must be < 2^31");
+    const size_t need = attn_packed_fwd_workspace_size(T, num_seqs, Hq, Hkv, D);
+    if (workspace_bytes < need)
+        return fail(ATTN_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
+    int dev = 0;
+    CUDA_TRY(cudaGetDevice(&dev));
+    PackedCall c{};
+    c.q = q;
+    c.k = k;
+    c.v = v;
+    c.qs = q_stride;
+    c.ks = k_stride;
+    c.vs = v_stride;
+    c.cu = cu_seqlens;
+    c.T = T;
+    c.S = num_seqs;
+    c.Hq = Hq;
+    c.Hkv = Hkv;
+    c.causal = causal;
+    c.window = window > 0 ? window : 0;
+    c.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D));
+    c.o = o;
+    c.lse = lse;
+    c.ws = workspace;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return D == 64 ? launch_packed<64, false>(c, s, dev) : launch_packed<128, false>(c, s, dev);
+}
+
+size_t attn_packed_bwd_workspace_size(int T, int num_seqs, int Hq, int D) {
+    if (T < 1 || num_seqs < 1 || Hq < 1 || D < 1) return 0;
+    return attn::bwd_plan_layout(T, num_seqs, Hq, D).total;
+}
+
+attn_status attn_packed_bwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, const void* o, const float* lse, const void* dout, void* dq, void* dk,
+                            void* dv, int64_t dq_stride, int64_t dk_stride, int64_t dv_stride,
+                            const int32_t* cu_seqlens, int num_seqs, int T, int Hq, int Hkv, int D, int causal,
+                            int window, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+    g_last_error.clear();
+    attn_status st = check_packed(T, num_seqs, Hq, Hkv, D, causal, window, scale);
+    if (st != ATTN_OK) return st;
+    if (T == 0) return ATTN_OK;
+    if ((st = check_rows("q", q, q_stride, Hq, D)) != ATTN_OK) return st;
+    if ((st = check_rows("k", k, k_stride, Hkv, D)) != ATTN_OK) return st;
+    if ((st = check_rows("v", v, v_stride, Hkv, D)) != ATTN_OK) return st;
+    if ((st = check_rows("dq", dq, dq_stride, Hq, D)) != ATTN_OK) return st;
+    if ((st = check_rows("dk", dk, dk_stride, Hkv, D)) != ATTN_OK) return st;
+    if ((st = check_rows("dv", dv, dv_stride, Hkv, D)) != ATTN_OK) return st;
+    if (!o || !lse || !dout || !workspace || !cu_seqlens)
+        return fail(ATTN_ERR_INVALID_ARG, "o, lse, dout, workspace and cu_seqlens must be non-NULL");
+    if (!aligned16(o) || !aligned16(dout) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return fail(ATTN_ERR_INVALID_ARG, "misaligned pointer (tensors 16-byte, int32/fp32 arrays 4-byte)");
+    if (too_many_rows(T, num_seqs, Hq)) return fail(ATTN_ERR_UNSUPPORTED, "too many rows: (T + 128 num_seqs) * Hq must be < 2^31");
+    const size_t need = attn_packed_bwd_workspace_size(T, num_seqs, Hq, D);
+    if (workspace_bytes < need)
+        return fail(ATTN_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
+    if (scale <= 0.f) scale = 1.0f / std::sqrt(static_cast<float>(D));
+    int dev = 0;
+    CUDA_TRY(cudaGetDevice(&dev));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    window = window > 0 ? window : 0;
+    return D == 64 ? launch_packed_bwd<64>(q, k, v, q_stride, k_stride, v_stride, o, lse, dout, dq, dk, dv, dq_stride,
+                                           dk_stride, dv_stride, cu_seqlens, num_seqs, T, Hq, Hkv, causal, window, scale,
+                                           workspace, s, dev)
+                   : launch_packed_bwd<128>(q, k, v, q_stride, k_stride, v_stride, o, lse, dout, dq, dk, dv, dq_stride,
+                                            dk_stride, dv_stride, cu_seqlens, num_seqs, T, Hq, Hkv, causal, window,
+                                            scale, workspace, s, dev);
+}
+
+size_t attn_chunk_workspace_size(int T, int num_seqs, int max_blocks_per_seq, int page_size, int Hq, int Hkv, int D) {
+    if (T < 1 || num_seqs < 1 || max_blocks_per_seq < 1 || page_size < 1 || Hq < 1 || Hkv < 1 || D < 1 ||
+        Hq % Hkv != 0 || Hq / Hkv > 128)
+        return 0;
+    return attn::plan_layout(T, num_seqs, 128 / (Hq / Hkv), static_cast<long long>(max_blocks_per_seq) * page_size, Hkv,
+                             D).total;
+}
+
+attn_status attn_chunk_paged(const void* q, const void* k_new, const void* v_new, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, void* k_pages, void* v_pages, const int32_t* block_table,
+                             const int32_t* seq_lens, const int32_t* cu_seqlens, int num_seqs, int T,
+                             int max_blocks_per_seq, int num_pages, int page_size, int Hq, int Hkv, int D, int window,
+                             float scale, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    g_last_error.clear();
+    attn_status st = check_packed(T, num_seqs, Hq, Hkv, D, 1, window, scale);
+    if (st != ATTN_OK) return st;
+    if (max_blocks_per_seq < 1 || num_pages < 1 || page_size < 1) return fail(ATTN_ERR_INVALID_ARG, "sizes must be >= 1");
+    if (page_size != attn::kPageSize) return fail(ATTN_ERR_UNSUPPORTED, "page_size %d not supported (16)", page_size);
+    if (static_cast<long long>(max_blocks_per_seq) * page_size >= (1 << 30))
+        return fail(ATTN_ERR_UNSUPPORTED, "max_blocks_per_seq * page_size must be < 2^30");
+    if (static_cast<double>(num_pages) * Hkv >= 2147483648.0 ||
+        static_cast<double>(num_pages) * Hkv * page_size * D * 2 >= 1099511627776.0)
+        return fail(ATTN_ERR_UNSUPPORTED, "KV pool larger than 1 TiB or 2^31 page slabs");
+    if ((k_new == nullptr) != (v_new == nullptr))
+        return fail(ATTN_ERR_INVALID_ARG, "k_new and v_new must both be given or both be NULL");
+    if (T == 0) return ATTN_OK;
+    if ((st = check_rows("q", q, q_stride, Hq, D)) != ATTN_OK) return st;
+    if (k_new != nullptr) {
+        if ((st = check_rows("k_new", k_new, k_stride, Hkv, D)) != ATTN_OK) return st;
+        if ((st = check_rows("v_new", v_new, v_stride, Hkv, D)) != ATTN_OK) return st;
+    }
+    if (!k_pages || !v_pages || !block_table || !seq_lens || !cu_seqlens || !o || !workspace)
+        return fail(ATTN_ERR_INVALID_ARG,
+                    "k_pages, v_pages, block_table, seq_lens, cu_seqlens, o and workspace must be non-NULL");
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !aligned16(workspace) ||
+        (reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return fail(ATTN_ERR_INVALID_ARG, "misaligned pointer (tensors 16-byte, int32/fp32 arrays 4-byte)");
+    if (too_many_rows(T, num_seqs, Hq)) return fail(ATTN_ERR_UNSUPPORTED, "too many rows: (T + 128 num_seqs) * Hq must be < 2^31");
+    const size_t need = attn_chunk_workspace_size(T, num_seqs, max_blocks_per_seq, page_size, Hq, Hkv, D);
+    if (workspace_bytes < need)
+        return fail(ATTN_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
+    int dev = 0;
+    CUDA_TRY(cudaGetDevice(&dev));
+    PackedCall c{};
+    c.q = q;
+    c.k = k_pages;
+    c.v = v_pages;
+    c.k_new = k_new;
+    c.v_new = v_new;
+    c.qs = q_stride;
+    c.ks = k_stride;
+    c.vs = v_stride;
+    c.cu = cu_seqlens;
+    c.seq_lens = seq_lens;
+    c.block_table = block_table;
+    c.T = T;
+    c.S = num_seqs;
+    c.Hq = Hq;
+    c.Hkv = Hkv;
+    c.causal = 1;
+    c.window = window > 0 ? window : 0;
+    c.max_blocks = max_blocks_per_seq;
+    c.num_pages = num_pages;
+    c.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D));
+    c.o = o;
+    c.lse = lse;
+    c.ws = workspace;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return D == 64 ? launch_packed<64, true>(c, s, dev) : launch_packed<128, true>(c, s, dev);
 }
 
 attn_status attn_get_device_status(void* stream, int* flags_out) {

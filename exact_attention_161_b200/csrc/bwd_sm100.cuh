@@ -24,6 +24,7 @@
 #pragma once
 #include "common.cuh"
 #include "fwd_sm100.cuh"
+#include "plan.cuh"
 #include "ptx.cuh"
 
 namespace attn {
@@ -43,29 +44,64 @@ struct BwdParams {
     int causal, window;
     float scale, scale_log2;
     int debug_drop_copy;        // test hook: CTA 0 skips its first Q / dO copy (see attn.h)
+    // Packed sequences (the kernels' kPacked forms): o and dout are [T, Hq, D], lse is [Hq, T]; the
+    // 128-row tiles of all sequences are numbered one behind the other, vec is [tiles, Hq, 2, 128] and
+    // dqacc [tiles, Hq, 128, D]; the gradients' rows are dq_stride, dk_stride, dv_stride elements apart.
+    const PlanHeader* header;
+    const PackedTile* tiles;
+    const int* order;           // tile numbers, most visible query tiles first
+    long long dq_stride, dk_stride, dv_stride;
+    int T;
 };
 
 // Per query row: -D_i = -(dO_i . O_i) and -LSE_i * log2(e), stored negated so that the kernels add
 // them, and the row's fp32 dq sums set to zero. D/8 lanes share a row (16-byte loads), grid-stride
 // over all padded rows; rows past N get (-inf, 0) so that their recomputed probabilities are
 // exactly 0.
-template <int D>
+// kPacked: the rows of a tile are walked token by token (the heads of a token lie side by side).
+template <int D, bool kPacked = false>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const BwdParams p) {
     constexpr int LPR = D / 8;     // lanes per row
     constexpr int RPW = 32 / LPR;  // rows per warp and pass
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
+    if constexpr (kPacked) {
+        ptx::grid_launch_dependents();
+        ptx::grid_dependency_wait();  // the plan
+    }
     const long long npad = static_cast<long long>(p.ntiles) * 128;
-    const long long rows = static_cast<long long>(p.B) * p.Hq * npad;
+    const long long rows = kPacked ? static_cast<long long>(p.header->n_items) * 128 * p.Hq
+                                   : static_cast<long long>(p.B) * p.Hq * npad;
     const long long nwarps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
     for (long long base = (static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * RPW;
          base < rows; base += nwarps * RPW) {
         const long long row = base + sub;
-        const long long bh = row / npad;
-        const int i = static_cast<int>(row - bh * npad);
-        const bool valid = row < rows && i < p.N;
+        bool valid;
+        size_t off = 0, lse_at = 0, zrow = static_cast<size_t>(row), vec_at;
+        if constexpr (kPacked) {
+            const long long tr = row / p.Hq;  // padded token: tile * 128 + i
+            const int h = static_cast<int>(row - tr * p.Hq), i = static_cast<int>(tr & 127);
+            valid = false;
+            if (row < rows) {
+                const PackedTile t = p.tiles[tr >> 7];
+                valid = t.t * 128 + i < t.n;
+                const size_t token = static_cast<size_t>(t.row0) + t.t * 128 + i;
+                off = (token * p.Hq + h) * D;
+                lse_at = static_cast<size_t>(h) * p.T + token;
+            }
+            const size_t th = static_cast<size_t>(tr >> 7) * p.Hq + h;
+            zrow = th * 128 + i;
+            vec_at = th * 256 + i;
+        } else {
+            const long long bh = row / npad;
+            const int i = static_cast<int>(row - bh * npad);
+            valid = row < rows && i < p.N;
+            off = (static_cast<size_t>(bh) * p.N + i) * D;
+            lse_at = static_cast<size_t>(bh) * p.N + i;
+            vec_at = (static_cast<size_t>(bh) * p.ntiles + i / 128) * 256 + (i & 127);
+        }
         float acc = 0.f;
         if (valid) {
-            const size_t off = (static_cast<size_t>(bh) * p.N + i) * D + l * 8;
+            off += l * 8;
             const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.o + off));
             const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.dout + off));
             const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
@@ -76,15 +112,15 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const BwdParams p) {
             }
         }
         if (row < rows) {
-            float4* z = reinterpret_cast<float4*>(p.dqacc + static_cast<size_t>(row) * D + l * 8);
+            float4* z = reinterpret_cast<float4*>(p.dqacc + zrow * D + l * 8);
             z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
             z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int m = LPR / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
         if (row < rows && l == 0) {
-            float* v = p.vec + (static_cast<size_t>(bh) * p.ntiles + i / 128) * 256 + (i & 127);
-            v[0] = valid ? -p.lse[static_cast<size_t>(bh) * p.N + i] * kLog2e : -INFINITY;
+            float* v = p.vec + vec_at;
+            v[0] = valid ? -p.lse[lse_at] * kLog2e : -INFINITY;
             v[128] = valid ? -acc : 0.f;
         }
     }
@@ -239,7 +275,14 @@ __device__ __forceinline__ uint32_t dq_box(int cg, int qw, const uint8_t* sQ, co
 // while they form dS^T(t+1). The ring stage that S^T(t+1) reads is held by the dQ reduce of two
 // steps back until the TMA has read it (about 64 KB at ~20 bytes per clock per SM under load), so
 // issuing it earlier in the step gains nothing.
-template <int D>
+//
+// kPacked: the CTA's key tile is the (block number / Hkv)-th of the plan's order, of a sequence of N
+// tokens whose rows start at row0 of the packed tensors. Rows behind the sequence's end belong to
+// another sequence or to nobody and may hold NaN: such queries and keys get P = dS = 0 by selection, and
+// where they are summed over (dV and dK over queries, dQ over keys) the product stops at the last
+// 16-row slice with a valid row, whose other rows are set to zero in shared memory by the
+// elementwise warps before P^T (dO) and dS^T (Q, K) are handed over.
+template <int D, bool kPacked = false>
 __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -257,14 +300,30 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                                                                       : reinterpret_cast<uint8_t*>(sVec) + 2 * C::VEC_BYTES);
     volatile int* abort_flag = &bar->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int groups = p.B * p.Hkv;
-    const int jt = static_cast<int>(blockIdx.x / groups);
-    const int gb = static_cast<int>(blockIdx.x - static_cast<unsigned>(jt) * groups);
-    const int g = gb % p.Hkv, b = gb / p.Hkv;
-    const int j0 = jt * 128;
     const int G = p.Hq / p.Hkv;
-    int ib, ie;
-    query_tiles_for_keys(j0, p.N, p.causal, p.window, ib, ie);
+    int ib, ie, j0, g, b = 0;
+    int N = p.N, row0 = 0, tile0 = 0;  // packed: the sequence's tokens, first row and first tile
+    if constexpr (kPacked) {
+        ptx::grid_launch_dependents();
+        ptx::grid_dependency_wait();  // the plan and the prep pass
+        const int entry = static_cast<int>(blockIdx.x / p.Hkv);
+        if (entry >= p.header->n_items) return;
+        g = static_cast<int>(blockIdx.x - static_cast<unsigned>(entry) * p.Hkv);
+        const PackedTile tile = p.tiles[p.order[entry]];
+        N = tile.n;
+        row0 = tile.row0;
+        tile0 = tile.base;
+        j0 = tile.t * 128;
+        query_tiles(tile.t, N, p.causal, p.window, ib, ie);
+    } else {
+        const int groups = p.B * p.Hkv;
+        const int jt = static_cast<int>(blockIdx.x / groups);
+        const int gb = static_cast<int>(blockIdx.x - static_cast<unsigned>(jt) * groups);
+        g = gb % p.Hkv;
+        b = gb / p.Hkv;
+        j0 = jt * 128;
+        query_tiles_for_keys(j0, p.N, p.causal, p.window, ib, ie);
+    }
     const int per_head = max(0, ie - ib);
     const int T = G * per_head;  // steps
 
@@ -302,8 +361,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             const int zk = b * p.Hkv + g;
             ptx::mbar_arrive_expect_tx(&bar->fixed_loaded, 2 * C::TILE_BYTES);
             for (int r = 0; r < C::NREG; ++r) {
-                ptx::tma_load_3d(sK + r * C::REGION_BYTES, &tm_k, &bar->fixed_loaded, r * 64, j0, zk);
-                ptx::tma_load_3d(sV + r * C::REGION_BYTES, &tm_v, &bar->fixed_loaded, r * 64, j0, zk);
+                const int c1 = kPacked ? g : j0, c2 = kPacked ? row0 + j0 : zk;
+                ptx::tma_load_3d(sK + r * C::REGION_BYTES, &tm_k, &bar->fixed_loaded, r * 64, c1, c2);
+                ptx::tma_load_3d(sV + r * C::REGION_BYTES, &tm_v, &bar->fixed_loaded, r * 64, c1, c2);
             }
             int issued = 0;
             bool ok = true;
@@ -314,14 +374,16 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                 const int zq = b * p.Hq + h;
                 ptx::mbar_arrive_expect_tx(&bar->full[s], 2 * C::TILE_BYTES + C::VEC_BYTES);
                 if (!(p.debug_drop_copy && t == 0 && blockIdx.x == 0)) {
+                    const int c1 = kPacked ? h : qt * 128, c2 = kPacked ? row0 + qt * 128 : zq;
                     for (int r = 0; r < C::NREG; ++r) {
-                        ptx::tma_load_3d(sQ + s * C::TILE_BYTES + r * C::REGION_BYTES, &tm_q, &bar->full[s], r * 64,
-                                         qt * 128, zq);
-                        ptx::tma_load_3d(sDO + s * C::TILE_BYTES + r * C::REGION_BYTES, &tm_do, &bar->full[s], r * 64,
-                                         qt * 128, zq);
+                        ptx::tma_load_3d(sQ + s * C::TILE_BYTES + r * C::REGION_BYTES, &tm_q, &bar->full[s], r * 64, c1,
+                                         c2);
+                        ptx::tma_load_3d(sDO + s * C::TILE_BYTES + r * C::REGION_BYTES, &tm_do, &bar->full[s], r * 64, c1,
+                                         c2);
                     }
-                    ptx::bulk_load(sVec + s * 256, p.vec + (static_cast<size_t>(zq) * p.ntiles + qt) * 256,
-                                   C::VEC_BYTES, &bar->full[s]);
+                    const size_t vec_tile = kPacked ? static_cast<size_t>(tile0 + qt) * p.Hq + h
+                                                    : static_cast<size_t>(zq) * p.ntiles + qt;
+                    ptx::bulk_load(sVec + s * 256, p.vec + vec_tile * 256, C::VEC_BYTES, &bar->full[s]);
                 }
                 issued = t + 1;
             }
@@ -374,27 +436,34 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                     ptx::mma_ss(tm + T_DP, ptx::desc64(v_lo + kslice(kk), HI), ptx::desc64(do_lo + st + kslice(kk), HI),
                                 ID_S, kk > 0);
             };
+            // 16-row slices of step t's query tile and of the key tile that hold a row of the sequence
+            auto query_slices = [&](int t) {
+                return kPacked ? min(8, (N - (ie - 1 - t / G) * 128 + 15) >> 4) : 8;
+            };
+            const int key_slices = kPacked ? min(8, (N - j0 + 15) >> 4) : 8;
             // dV += P^T dO (M = 128 keys, N = D, K = 128 queries; P^T packed in TMEM)
             auto issue_dv = [&](int t) {
                 const uint32_t st = (t & 1) * TILE16;
+                const int slices = query_slices(t);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    ptx::mma_ts(tm + T_DV, tm + T_S + packed_col(kk), ptx::desc64(domn_lo + st + kk * 128, HI), ID_G,
+                    if (!kPacked || kk < slices) ptx::mma_ts(tm + T_DV, tm + T_S + packed_col(kk), ptx::desc64(domn_lo + st + kk * 128, HI), ID_G,
                                 (t > 0 || kk > 0) ? 1u : 0u);
             };
             // dK += dS^T Q (M = 128 keys, N = D, K = 128 queries)
             auto issue_dk = [&](int t) {
                 const uint32_t st = (t & 1) * TILE16;
+                const int slices = query_slices(t);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    ptx::mma_ss(tm + T_DK, ptx::desc64(ds_lo + kslice(kk), HI), ptx::desc64(qmn_lo + st + kk * 128, HI),
+                    if (!kPacked || kk < slices) ptx::mma_ss(tm + T_DK, ptx::desc64(ds_lo + kslice(kk), HI), ptx::desc64(qmn_lo + st + kk * 128, HI),
                                 ID_G, (t > 0 || kk > 0) ? 1u : 0u);
             };
             // dQ partial = dS K (M = 128 queries, N = D, K = 128 keys), into the dP^T columns
             auto issue_dq = [&]() {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    ptx::mma_ss(tm + T_DP, ptx::desc64(dsmn_lo + kk * 128, HI), ptx::desc64(kmn_lo + kk * 128, HI), ID_Q,
+                    if (!kPacked || kk < key_slices) ptx::mma_ss(tm + T_DP, ptx::desc64(dsmn_lo + kk * 128, HI), ptx::desc64(kmn_lo + kk * 128, HI), ID_Q,
                                 kk > 0);
             };
             bool ok = ptx::mbar_wait_warp(&bar->fixed_loaded, 0, abort_flag) &&
@@ -461,12 +530,14 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                 const int s = t & 1;
                 const int qt = ie - 1 - t / G, h = g * G + t % G;
                 if (!ptx::mbar_wait(&bar->staged[s], (t >> 1) & 1, abort_flag)) { ok = false; break; }
-                const int row0 = ((b * p.Hq + h) * p.ntiles + qt) * 128;
+                const int acc_row = (kPacked ? (tile0 + qt) * p.Hq + h : (b * p.Hq + h) * p.ntiles + qt) * 128;
+                const int boxes = kPacked ? min(4, (N - qt * 128 + 31) >> 5) : 4;  // 32-row boxes with a valid row
 #pragma unroll 1
                 for (int cg = 0; cg < D / 32; ++cg)
 #pragma unroll
                     for (int qw = 0; qw < 4; ++qw)
-                        ptx::tma_reduce_add_2d(&tm_dq, dq_box<D>(cg, qw, sQ, sDO, s), 32 * cg, row0 + 32 * qw);
+                        if (!kPacked || qw < boxes)
+                            ptx::tma_reduce_add_2d(&tm_dq, dq_box<D>(cg, qw, sQ, sDO, s), 32 * cg, acc_row + 32 * qw);
                 ptx::bulk_commit_group();
                 ptx::bulk_wait_read<0>();
                 ptx::mbar_arrive(&bar->empty[s]);
@@ -504,8 +575,34 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             }
             // query qpos sees this key iff qpos >= key (causal) and qpos - key < window
             const int lo = p.causal ? key - c0 : -1;
-            const int hi = p.window > 0 ? key + p.window - 1 - c0 : 32;
+            int hi = p.window > 0 ? key + p.window - 1 - c0 : 32;
+            bool past_end = false;  // packed: a query column or the key row lies behind the sequence
+            if constexpr (kPacked) {
+                if (p.window > 0) hi = p.window >= N ? 32 : hi;  // (key + window stays an int)
+                past_end = key >= N || c0 + 32 > N;
+                if (past_end) hi = key >= N ? -1 : min(hi, N - 1 - c0);
+            }
             if (lo > 0 || hi < 31) mask32(pr, lo, hi);
+            if constexpr (kPacked) {
+                // zero the rows behind the sequence in the last slice that the products read
+                auto zero_rows = [&](uint8_t* tile, int rows) {
+                    const int chunks = (16 - (rows & 15)) * 8;  // 16-byte pieces per region
+                    const uint32_t base = ptx::smem_u32(tile) + rows * 128;
+                    for (int e = threadIdx.x; e < chunks * C::NREG; e += C::EW_THREADS)
+                        ptx::st_shared_v4(base + (e / chunks) * C::REGION_BYTES + (e % chunks) * 16, 0, 0, 0, 0);
+                };
+                const int q_rows = N - qt * 128, k_rows = N - j0;
+                const bool q_tail = q_rows < 128 && (q_rows & 15), k_tail = t == 0 && k_rows < 128 && (k_rows & 15);
+                if (q_tail) {
+                    zero_rows(sQ + s * C::TILE_BYTES, q_rows);
+                    zero_rows(sDO + s * C::TILE_BYTES, q_rows);
+                }
+                if (k_tail) {
+                    if (!ptx::mbar_wait(&bar->fixed_loaded, 0, abort_flag)) { ok = false; break; }
+                    zero_rows(sK, k_rows);
+                }
+                if (q_tail || k_tail) ptx::fence_proxy_async_smem();
+            }
             {
                 uint32_t pk[16];
 #pragma unroll
@@ -520,6 +617,15 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                 uint32_t dp[32], dsk[16];
                 ptx::tmem_ld32(t_dp, dp);
                 dscores32_cols(pr, dp, vec + 128, dsk);
+                if constexpr (kPacked) {
+                    if (past_end) {  // dP may be NaN there: select, as for P
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const uint32_t keep = (2 * c <= hi ? 0x0000FFFFu : 0u) | (2 * c + 1 <= hi ? 0xFFFF0000u : 0u);
+                            dsk[c] &= keep;
+                        }
+                    }
+                }
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     ptx::st_shared_v4(ds_row + ((((cg & 1) * 4 + c) ^ (r & 7)) << 4), dsk[4 * c], dsk[4 * c + 1],
@@ -552,21 +658,25 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         if (ok && T > 0) {
             // every lane takes part in the warp-collective TMEM loads; rows past N store nothing
             ptx::tc_fence_after();
-            const size_t row = (static_cast<size_t>(b) * p.Hkv + g) * p.N + min(key, p.N - 1);
+            const size_t row = (static_cast<size_t>(b) * p.Hkv + g) * N + min(key, N - 1);
+            const size_t token = static_cast<size_t>(row0) + min(key, N - 1);
+            __nv_bfloat16* out_k = p.dk + (kPacked ? token * p.dk_stride + g * D : row * D);
+            __nv_bfloat16* out_v = p.dv + (kPacked ? token * p.dv_stride + g * D : row * D);
 #pragma unroll 1
             for (int c = 0; c < D / 64; ++c) {
                 uint32_t v[32];
                 ptx::tmem_ld32(tmem + lane_base + (is_k ? T_DK : T_DV) + col0 + c * 32, v);
-                if (key < p.N) {
+                if (key < N) {
                     if (is_k)
-                        store_chunk_unrotated(v, p.scale, p.rope, D, key, col0 + c * 32, p.dk + row * D);
+                        store_chunk_unrotated(v, p.scale, kPacked ? nullptr : p.rope, D, key, col0 + c * 32, out_k);
                     else
-                        store_chunk_unrotated(v, 1.f, nullptr, D, key, col0 + c * 32, p.dv + row * D);
+                        store_chunk_unrotated(v, 1.f, nullptr, D, key, col0 + c * 32, out_v);
                 }
             }
-        } else if (T == 0 && key < p.N) {
-            // no query sees these keys: zero gradients
-            const size_t row = (static_cast<size_t>(b) * p.Hkv + g) * p.N + key;
+        } else if (!kPacked && T == 0 && key < N) {
+            // no query sees these keys: zero gradients (packed sequences attend to themselves: every
+            // key is seen)
+            const size_t row = (static_cast<size_t>(b) * p.Hkv + g) * N + key;
             uint4* d1 = reinterpret_cast<uint4*>((is_k ? p.dk : p.dv) + row * D + col0);
             for (int k = 0; k < D / 16; ++k) d1[k] = make_uint4(0, 0, 0, 0);
         }
@@ -613,6 +723,30 @@ __global__ void __launch_bounds__(256) bwd_dq_store_kernel(const BwdParams p) {
         *reinterpret_cast<uint4*>(p.dq + static_cast<size_t>(row) * D + c0) =
             make_uint4(ptx::pack_bf16x2(g[0], g[1]), ptx::pack_bf16x2(g[2], g[3]), ptx::pack_bf16x2(g[4], g[5]),
                        ptx::pack_bf16x2(g[6], g[7]));
+    }
+}
+
+// The same for packed sequences: the rows of a tile token by token, stored dq_stride elements apart.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_dq_store_packed_kernel(const BwdParams p) {
+    ptx::grid_dependency_wait();
+    constexpr int CPR = D / 8;
+    const long long total = static_cast<long long>(p.header->n_items) * 128 * p.Hq * CPR;
+    for (long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; idx < total;
+         idx += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const long long row = idx / CPR;
+        const int c0 = static_cast<int>(idx - row * CPR) * 8;
+        const long long tr = row / p.Hq;
+        const int h = static_cast<int>(row - tr * p.Hq), i = static_cast<int>(tr & 127);
+        const PackedTile t = p.tiles[tr >> 7];
+        if (t.t * 128 + i >= t.n) continue;
+        const float4* src =
+            reinterpret_cast<const float4*>(p.dqacc + ((static_cast<size_t>(tr >> 7) * p.Hq + h) * 128 + i) * D + c0);
+        const float4 a = src[0], c = src[1];
+        const size_t token = static_cast<size_t>(t.row0) + t.t * 128 + i;
+        *reinterpret_cast<uint4*>(p.dq + token * p.dq_stride + h * D + c0) =
+            make_uint4(ptx::pack_bf16x2(a.x * p.scale, a.y * p.scale), ptx::pack_bf16x2(a.z * p.scale, a.w * p.scale),
+                       ptx::pack_bf16x2(c.x * p.scale, c.y * p.scale), ptx::pack_bf16x2(c.z * p.scale, c.w * p.scale));
     }
 }
 

@@ -9,6 +9,7 @@ enum : unsigned int {
     kStatusTimeout = 1u,      // a bounded pipeline wait gave up (the CTA bailed out)
     kStatusBadPage = 2u,      // a block-table entry outside [0, num_pages) was skipped
     kStatusBadSeqLen = 4u,    // a seq_len outside [1, max_blocks * page_size) was skipped
+    kStatusBadOffsets = 8u,   // offsets of packed sequences that decrease or leave [0, T]: nothing was computed
 };
 
 // One word per device: the only state the kernels share across launches. The library is a

@@ -1,0 +1,840 @@
+// packed_sm100.cuh -- attention over packed sequences of different lengths, and over chunks of new
+// tokens on a paged KV cache, for sm_100a.
+//
+// Tokens of all sequences lie one behind the other (token-major [T, H, D] rows); sequence s owns
+// rows [cu[s], cu[s+1]) of the queries. Its keys are its own rows (packed) or its pages of the cache
+// (paged), of which its queries are the last ones. Per row the computation is the online softmax of
+// fwd_sm100.cuh; what differs is how work is cut and fed:
+//
+//   Rows.  A query tile's 128 rows are TT = 128 / G tokens times the G query heads of one K/V head
+//     (row r = token r / G, head r % G), loaded by one TMA box of {64 columns, G heads, TT tokens} per
+//     128-byte region. Short sequences and single tokens then fill G times more of a tile, and a
+//     K/V tile is read once for the whole group. (G that does not divide 128 leaves 128 - G TT rows
+//     of every tile unused: 2 for G = 3, 8 for G = 5.)
+//   Items. The list of plan.cuh, walked by one persistent CTA per SM, longest items first.
+//   Parts. A block whose keys were cut into parts writes fp32 partial states that
+//     packed_merge_kernel joins in ascending order.
+//   Pages. A 128-key tile of the cache is eight 16-token pages, each fetched by its own box; lane i
+//     of the producer warp looks up and issues page i.
+//   Tails. A sequence ends inside a key tile; the rows behind its end belong to another sequence or
+//     to nobody and may hold NaN. Scores are masked by selection. For P V, 0 * NaN would survive, so
+//     the product stops at the last 16-key slice with a visible key (one MMA per slice), and the
+//     rest of that slice's V rows are set to zero in shared memory by the softmax warps before P is
+//     handed over.
+//
+// The roles, TMEM layout, issue order and softmax arithmetic are those of attn_fwd_kernel.
+#pragma once
+#include "common.cuh"
+#include "fwd_sm100.cuh"
+#include "plan.cuh"
+#include "ptx.cuh"
+
+namespace attn {
+
+struct PlanParams {
+    const int32_t* cu;        // [S + 1] offsets of the packed tokens
+    const int32_t* seq_lens;  // paged: [S] keys of every sequence (its new tokens among them); packed: nullptr
+    PlanHeader* header;
+    int* prefix;              // [S + 1] blocks (backward: tiles) of the sequences before each
+    PackedItem* items;
+    SplitBlock* split;
+    PackedTile* tiles;        // backward: natural order
+    int* order;               // backward: tile numbers, most query tiles first
+    int S, T, TT, Hkv, causal, window;
+    int max_len;              // paged: tokens a block-table row can hold
+    int max_slots;
+};
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanSmemSeqs = 2048;  // the prefix sums are searched in shared memory up to this many sequences
+
+// Exclusive scan over the CTA; every thread gets the total. `warp_sums`: 33 ints of shared memory.
+__device__ __forceinline__ int plan_scan(int x, int* warp_sums, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += y;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        const int v = warp_sums[lane];
+        int w = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, d);
+            if (lane >= d) w += y;
+        }
+        warp_sums[lane] = w - v;
+        if (lane == 31) warp_sums[32] = w;
+    }
+    __syncthreads();
+    total = warp_sums[32];
+    const int out = warp_sums[warp] + inc - x;
+    __syncthreads();
+    return out;
+}
+
+// Builds the item list (one CTA). kBwd: the backward's tiles. Three walks over the blocks: the sum
+// and the largest of their key tiles (the split rule), the histogram, the list. Runs in a few
+// microseconds; what it costs is the latency of its steps, not the number of blocks.
+template <bool kBwd>
+__device__ void build_plan(const PlanParams& p) {
+    __shared__ int s_hist[kPlanBuckets];
+    __shared__ int s_prefix[kPlanSmemSeqs + 1];
+    __shared__ int s_warp[33];
+    __shared__ unsigned long long s_sum;
+    __shared__ int s_max, s_slots, s_split;
+    const int tid = threadIdx.x;
+    const int tok = kBwd ? 128 : 2 * p.TT;  // tokens per block
+    int* pre = p.S <= kPlanSmemSeqs ? s_prefix : p.prefix;
+    if (tid == 0) {
+        s_sum = 0;
+        s_max = 1;
+        s_slots = s_split = 0;
+    }
+    s_hist[tid] = 0;
+    int carry = 0, bad = 0;
+    for (int base = 0; base < p.S; base += kPlanThreads) {
+        const int s = base + tid;
+        int blocks = 0;
+        if (s < p.S) {
+            const int a = p.cu[s], b = p.cu[s + 1];
+            if (a < 0 || b < a || b > p.T)
+                bad = 1;
+            else
+                blocks = plan_ceil(b - a, tok);
+        }
+        int total;
+        const int at = plan_scan(blocks, s_warp, total);
+        if (s < p.S) pre[s] = carry + at;
+        // T < 2^30 bounds the sum of valid offsets; with invalid ones it may pass 2^31, and the list is not built
+        carry += total;
+    }
+    bad = __syncthreads_or(bad);
+    const int n_blocks = bad ? 0 : carry;
+    if (tid == 0) pre[p.S] = n_blocks;
+    if (bad) {
+        if (tid == 0) {
+            raise_status(kStatusBadOffsets);
+            PlanHeader h{0, 0, 1, 0};
+            *p.header = h;
+        }
+        return;
+    }
+    __syncthreads();
+
+    struct Block {
+        int s, first, n, tiles, kv_len;  // sequence, first token and tokens of the block, its tiles, keys
+    };
+    auto block_of = [&](int b) {
+        int lo = 0, hi = p.S - 1;  // the last sequence whose first block is <= b (empty ones never are the last)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (pre[mid] <= b)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        Block x;
+        x.s = lo;
+        const int n = p.cu[lo + 1] - p.cu[lo];
+        x.first = (b - pre[lo]) * tok;
+        x.n = min(tok, n - x.first);
+        if constexpr (kBwd) {
+            int ib, ie;
+            query_tiles(b - pre[lo], n, p.causal, p.window, ib, ie);
+            x.tiles = max(0, ie - ib);
+            x.kv_len = n;
+        } else {
+            int len = n;
+            if (p.seq_lens != nullptr) {
+                len = p.seq_lens[lo];
+                if (len < n || len > p.max_len) len = -1;
+            }
+            x.kv_len = len;
+            const int pos = len - n + x.first;
+            x.tiles = len < 0 ? 0 : key_tiles(pos, pos + x.n - 1, len, p.causal, p.window).n;
+        }
+        return x;
+    };
+    Block mine{};  // this thread's first block is kept; further ones are looked up again in each walk
+    if (tid < n_blocks) mine = block_of(tid);
+    auto get = [&](int b) { return b == tid ? mine : block_of(b); };
+
+    long long sum = 0;
+    int most = 1;
+    for (int b = tid; b < n_blocks; b += kPlanThreads) {
+        const Block x = get(b);
+        sum += x.tiles;
+        most = max(most, x.tiles);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if ((tid & 31) == 0 && tid < n_blocks) {
+        atomicAdd(&s_sum, static_cast<unsigned long long>(sum));
+        atomicMax(&s_max, most);
+    }
+    __syncthreads();
+    const int limit = kBwd ? 0x3fffffff : plan_limit(static_cast<long long>(s_sum), p.Hkv);
+    const int longest = s_max;
+    auto bucket = [&](int tiles) {
+        return kPlanBuckets - 1 - static_cast<int>(static_cast<long long>(tiles) * (kPlanBuckets - 1) / longest);
+    };
+    auto parts_of = [&](const Block& x) { return kBwd ? 1 : plan_parts(x.tiles, limit); };
+
+    for (int b = tid; b < n_blocks; b += kPlanThreads) {
+        const Block x = get(b);
+        const int parts = parts_of(x), q = x.tiles / parts, r = x.tiles % parts;
+        if (r > 0) atomicAdd(&s_hist[bucket(q + 1)], r);
+        atomicAdd(&s_hist[bucket(q)], parts - r);
+    }
+    __syncthreads();
+    int n_items;
+    const int start = plan_scan(s_hist[tid], s_warp, n_items);
+    s_hist[tid] = start;
+    __syncthreads();
+
+    for (int b = tid; b < n_blocks; b += kPlanThreads) {
+        const Block x = get(b);
+        if constexpr (kBwd) {
+            PackedTile t;
+            t.row0 = p.cu[x.s];
+            t.n = x.kv_len;
+            t.base = pre[x.s];
+            t.t = b - t.base;
+            p.tiles[b] = t;
+            p.order[atomicAdd(&s_hist[bucket(x.tiles)], 1)] = b;
+        } else {
+            const int parts = parts_of(x);
+            const int row0 = p.cu[x.s];
+            const int n = p.cu[x.s + 1] - row0;
+            PackedItem it;
+            it.q_row = row0 + x.first;
+            it.pos0 = x.kv_len < 0 ? 0 : x.kv_len - n + x.first;
+            it.kv = p.seq_lens != nullptr ? x.s : row0;
+            it.kv_len = x.kv_len;
+            it.slot = 0;
+            if (parts > 1) {
+                it.slot = atomicAdd(&s_slots, parts);
+                p.split[atomicAdd(&s_split, 1)] = SplitBlock{it.q_row, x.n, it.slot, parts};
+            }
+            const int jb =
+                x.kv_len < 0 ? 0 : key_tiles(it.pos0, it.pos0 + x.n - 1, x.kv_len, p.causal, p.window).jb;
+            for (int i = 0; i < parts; ++i) {
+                int b0, b1;
+                plan_part(x.tiles, parts, i, b0, b1);
+                it.jb = jb + b0;
+                it.n_tiles = b1 - b0;
+                it.meta = make_meta(x.n, i, parts);
+                p.items[atomicAdd(&s_hist[bucket(it.n_tiles)], 1)] = it;
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        PlanHeader h{n_items, s_split, 0, 0};
+        *p.header = h;
+    }
+}
+
+// Chunks on the paged cache: new token t of sequence s goes to page block_table[s][pos / 16], slot
+// pos % 16, pos = seq_lens[s] - n_s + t.
+struct AppendParams {
+    const __nv_bfloat16* k_new;  // [T, Hkv, D] (token stride ks), or nullptr (nothing to append)
+    const __nv_bfloat16* v_new;
+    __nv_bfloat16* k_pages;      // [num_pages, Hkv, 16, D]
+    __nv_bfloat16* v_pages;
+    const int32_t* block_table;
+    long long ks, vs;
+    int max_blocks, num_pages;
+};
+
+// Block 0 builds the plan; with kPaged the other blocks append the new tokens meanwhile, a warp per
+// (token, K/V head): 2 D elements each way.
+template <int D, bool kPaged, bool kBwd>
+__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PlanParams p, const AppendParams a) {
+    ptx::grid_launch_dependents();  // the attention kernel's set-up may overlap; it waits for this grid
+    if (blockIdx.x == 0) {
+        build_plan<kBwd>(p);
+        return;
+    }
+    if constexpr (kPaged) {
+        const int lane = threadIdx.x & 31;
+        const long long warps = static_cast<long long>(gridDim.x - 1) * (kPlanThreads / 32);
+        const long long rows = static_cast<long long>(p.T) * p.Hkv;
+        constexpr int LPR = D / 8;  // lanes per row of 16-byte pieces
+        for (long long w = static_cast<long long>(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5); w < rows;
+             w += warps) {
+            const int t = static_cast<int>(w / p.Hkv), g = static_cast<int>(w % p.Hkv);
+            // the sequence of token t: the last s with cu[s] <= t (invalid offsets end anywhere in [0, S))
+            int lo = 0, hi = p.S - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.cu[mid] <= t)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int c0 = p.cu[lo], c1 = p.cu[lo + 1], len = p.seq_lens[lo];
+            if (t < c0 || t >= c1 || c0 < 0 || c1 > p.T) continue;       // behind the last sequence
+            if (len < c1 - c0 || len > p.max_len) continue;              // flagged by the plan's user
+            const int pos = len - (c1 - t);
+            const int page = a.block_table[static_cast<size_t>(lo) * a.max_blocks + pos / kPageSize];
+            if (page < 0 || page >= a.num_pages) {
+                if (lane == 0) raise_status(kStatusBadPage);
+                continue;
+            }
+            const size_t dst = ((static_cast<size_t>(page) * p.Hkv + g) * kPageSize + pos % kPageSize) * D;
+            if (lane < 2 * LPR) {
+                const bool is_v = lane >= LPR;
+                const int c = is_v ? lane - LPR : lane;
+                const __nv_bfloat16* src = (is_v ? a.v_new + t * a.vs : a.k_new + t * a.ks) + static_cast<size_t>(g) * D;
+                __nv_bfloat16* out = (is_v ? a.v_pages : a.k_pages) + dst;
+                reinterpret_cast<uint4*>(out)[c] = __ldg(reinterpret_cast<const uint4*>(src) + c);
+            }
+        }
+    }
+}
+
+struct PackedParams {
+    const PlanHeader* header;
+    const PackedItem* items;
+    const int32_t* block_table;  // paged
+    __nv_bfloat16* o;            // [T, Hq, D]
+    float* lse;                  // element (token t, head h) at t * lse_t + h * lse_h, or nullptr
+    float* ws_ml;                // partial states: [slot][Hkv][256 rows][2] (max in log2 units, sum)
+    float* ws_o;                 // [slot][Hkv][256 rows][D] unnormalised
+    long long lse_t, lse_h;
+    int Hq, Hkv, G, TT;
+    int causal, window;
+    int max_blocks, num_pages;   // paged
+    float scale_log2;
+    int debug_drop_copy;         // test hook: CTA 0 skips its first key-tile copy (see attn.h)
+};
+
+// An item of the list for one K/V head, with the key-tile range of each of its two query tiles.
+struct PackedWork {
+    int q_row, pos0, kv, kv_len, n_tok, part, parts, slot, g;
+    int J0, T;          // key tiles of the item
+    int tok[2];         // tokens of query tile i (0: absent)
+    int a[2], e[2];     // visible key tiles of query tile i: [J0 + a, J0 + e)
+};
+
+__device__ __forceinline__ PackedWork make_work(const PackedParams& p, int it) {
+    PackedWork w;
+    const int entry = it / p.Hkv;
+    w.g = it - entry * p.Hkv;
+    const int4* rec = reinterpret_cast<const int4*>(p.items + entry);
+    const int4 lo = rec[0], hi = rec[1];
+    w.q_row = lo.x;
+    w.pos0 = lo.y;
+    w.kv = lo.z;
+    w.kv_len = lo.w;
+    w.J0 = hi.x;
+    w.T = hi.y;
+    w.n_tok = hi.z & 1023;
+    w.part = (hi.z >> 10) & 1023;
+    w.parts = ((hi.z >> 20) & 1023) + 1;
+    w.slot = hi.w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int n = min(p.TT, w.n_tok - i * p.TT);
+        w.tok[i] = max(0, n);
+        w.a[i] = w.e[i] = 0;
+        if (n > 0 && w.T > 0) {
+            const int first = w.pos0 + i * p.TT;
+            const KeyTiles k = key_tiles(first, first + n - 1, w.kv_len, p.causal, p.window);
+            const int a = max(0, k.jb - w.J0), e = min(w.T, k.jb + k.n - w.J0);
+            if (e > a) {
+                w.a[i] = a;
+                w.e[i] = e;
+            }
+        }
+    }
+    return w;
+}
+
+template <int D, bool kPaged>
+__global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
+    attn_packed_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const PackedParams p) {
+    using C = FwdCfg<D>;
+    constexpr int NK = C::NK, NV = C::NV;
+    constexpr int kPages = C::BN / kPageSize;  // pages of a key tile
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sQ = smem;
+    uint8_t* sK = sQ + C::QT * C::TILE_BYTES;
+    uint8_t* sV = sK + NK * C::TILE_BYTES;
+    auto* bar = reinterpret_cast<FwdBarriers<NK, NV>*>(sV + NV * C::TILE_BYTES);
+    volatile int* abort_flag = &bar->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&bar->q_loaded[i], 1);
+            ptx::mbar_init(&bar->q_empty[i], 1);
+            ptx::mbar_init(&bar->s_full[i], 1);
+            ptx::mbar_init(&bar->p_full[i], 128);
+            ptx::mbar_init(&bar->o_final[i], 1);
+            ptx::mbar_init(&bar->o_empty[i], 128);
+        }
+        for (int s = 0; s < NK; ++s) {
+            ptx::mbar_init(&bar->k_full[s], 1);
+            ptx::mbar_init(&bar->k_empty[s], 1);
+        }
+        for (int s = 0; s < NV; ++s) {
+            ptx::mbar_init(&bar->v_full[s], 1);
+            ptx::mbar_init(&bar->v_empty[s], 1);
+        }
+        ptx::mbar_init(&bar->drain, 1);
+        bar->abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == C::PRODUCER_WARP && lane == 0) {
+        ptx::prefetch_tensormap(&tm_q);
+        ptx::prefetch_tensormap(&tm_k);
+        ptx::prefetch_tensormap(&tm_v);
+    }
+    if (warp == C::MMA_WARP) {
+        ptx::tmem_alloc(&bar->tmem_base, C::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();  // the plan (and the appended tokens)
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = bar->tmem_base;
+    const int n_items = p.header->n_items * p.Hkv;
+
+    if (warp == C::PRODUCER_WARP) {
+        // ------------------------------------------------------------------ TMA producer
+        // The whole warp walks the items. Lane 0 expects the bytes; the boxes of a packed tile are
+        // issued by lane 0, those of a paged tile by the lane that looked the page up.
+        int kq[2] = {0, 0};
+        int g = 0, k_issued = 0, v_issued = 0;
+        bool ok = true;
+        for (int rnd = 0, it = blockIdx.x; ok && it < n_items; it = item_of_round(++rnd, blockIdx.x, gridDim.x)) {
+            const PackedWork x = make_work(p, it);
+            for (int i = 0; i < 2 && ok; ++i) {
+                if (x.e[i] == x.a[i]) continue;
+                if (kq[i] > 0 && !ptx::mbar_wait_warp(&bar->q_empty[i], (kq[i] - 1) & 1, abort_flag)) { ok = false; break; }
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&bar->q_loaded[i], static_cast<uint32_t>(p.G * p.TT * C::ROW_BYTES));
+#pragma unroll
+                    for (int r = 0; r < C::NREG; ++r)
+                        ptx::tma_load_3d(sQ + i * C::TILE_BYTES + r * C::REGION_BYTES, &tm_q, &bar->q_loaded[i], r * 64,
+                                         x.g * p.G, x.q_row + i * p.TT);
+                }
+                ++kq[i];
+            }
+            const int32_t* bt = kPaged ? p.block_table + static_cast<size_t>(x.kv) * p.max_blocks : nullptr;
+            const int seq_pages = kPaged ? (x.kv_len + kPageSize - 1) / kPageSize : 0;
+            // pages before the window of the item's first token may have been given back: not looked up
+            const int first_page = p.window > 0 ? max(0, x.pos0 - p.window + 1) / kPageSize : 0;
+            // lane i of a paged tile: page i of the next tile, looked up one tile ahead
+            int page = 0;
+            auto look_up = [&](int u) {
+                const int pg = (x.J0 + u) * kPages + lane;
+                return (lane < kPages && u < x.T && pg < seq_pages && pg >= first_page) ? bt[pg] : -1;
+            };
+            if constexpr (kPaged) page = look_up(0);
+            for (int u = 0; u < x.T && ok; ++u, ++g) {
+                const int k0 = (x.J0 + u) * C::BN;
+                const int sk = g % NK, sv = g % NV;
+                if (g >= NK && !ptx::mbar_wait_warp(&bar->k_empty[sk], ((g / NK) - 1) & 1, abort_flag)) { ok = false; break; }
+                const bool drop = p.debug_drop_copy && g == 0 && blockIdx.x == 0;
+                int z = 0, pages = 0;
+                if constexpr (kPaged) {
+                    pages = min(kPages, seq_pages - (x.J0 + u) * kPages);
+                    // a page that is invalid (flagged) or before the window is read as zeros, by a box
+                    // outside the tensor: what its memory holds cannot reach a product
+                    const bool valid = page >= 0 && page < p.num_pages;
+                    if (lane < pages && !valid && (x.J0 + u) * kPages + lane >= first_page) raise_status(kStatusBadPage);
+                    z = valid ? page * p.Hkv + x.g : -1;
+                    page = look_up(u + 1);
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(&bar->k_full[sk], pages * kPageSize * C::ROW_BYTES);
+                    __syncwarp();
+                    if (lane < pages && !drop) {
+#pragma unroll
+                        for (int r = 0; r < C::NREG; ++r)
+                            ptx::tma_load_3d(sK + sk * C::TILE_BYTES + r * C::REGION_BYTES + lane * kPageSize * 128, &tm_k,
+                                             &bar->k_full[sk], r * 64, 0, z);
+                    }
+                } else if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&bar->k_full[sk], C::TILE_BYTES);
+                    if (!drop) {
+#pragma unroll
+                        for (int r = 0; r < C::NREG; ++r)
+                            ptx::tma_load_3d(sK + sk * C::TILE_BYTES + r * C::REGION_BYTES, &tm_k, &bar->k_full[sk], r * 64,
+                                             x.g, x.kv + k0);
+                    }
+                }
+                k_issued = g + 1;
+                if (g >= NV && !ptx::mbar_wait_warp(&bar->v_empty[sv], ((g / NV) - 1) & 1, abort_flag)) { ok = false; break; }
+                if constexpr (kPaged) {
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(&bar->v_full[sv], pages * kPageSize * C::ROW_BYTES);
+                    __syncwarp();
+                    if (lane < pages) {
+#pragma unroll
+                        for (int r = 0; r < C::NREG; ++r)
+                            ptx::tma_load_3d(sV + sv * C::TILE_BYTES + r * C::REGION_BYTES + lane * kPageSize * 128, &tm_v,
+                                             &bar->v_full[sv], r * 64, 0, z);
+                    }
+                } else if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&bar->v_full[sv], C::TILE_BYTES);
+#pragma unroll
+                    for (int r = 0; r < C::NREG; ++r)
+                        ptx::tma_load_3d(sV + sv * C::TILE_BYTES + r * C::REGION_BYTES, &tm_v, &bar->v_full[sv], r * 64, x.g,
+                                         x.kv + k0);
+                }
+                v_issued = g + 1;
+            }
+        }
+        if (!ok && lane == 0) {
+            *abort_flag = 1;
+            raise_status(kStatusTimeout);
+            // let the copies in flight land before the CTA's shared memory is released (bounded)
+            volatile int never = 0;
+            for (int i = 0; i < 2; ++i)
+                if (kq[i] > 0) ptx::mbar_wait(&bar->q_loaded[i], (kq[i] - 1) & 1, &never);
+            for (int u = max(0, k_issued - NK); u < k_issued; ++u) ptx::mbar_wait(&bar->k_full[u % NK], (u / NK) & 1, &never);
+            for (int u = max(0, v_issued - NV); u < v_issued; ++u) ptx::mbar_wait(&bar->v_full[u % NV], (u / NV) & 1, &never);
+        }
+        __syncwarp();
+    } else if (warp == C::MMA_WARP) {
+        // ------------------------------------------------------------------ MMA issuer
+        const uint32_t issue = ptx::elect_one() ? 1u : 0u;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, C::BN, 0, 0);
+        constexpr uint32_t IDESC_O = ptx::idesc_bf16_f32(128, D, 0, 1);
+        constexpr uint32_t HI = ptx::sw128_desc_hi(1024);
+        constexpr uint64_t TILE16 = C::TILE_BYTES >> 4;
+        const uint64_t q_d = ptx::desc64(__shfl_sync(0xffffffffu, ptx::sw128_desc_lo(ptx::smem_u32(sQ), 16), 0), HI);
+        const uint64_t k_d = ptx::desc64(__shfl_sync(0xffffffffu, ptx::sw128_desc_lo(ptx::smem_u32(sK), 16), 0), HI);
+        const uint64_t v_d =
+            ptx::desc64(__shfl_sync(0xffffffffu, ptx::sw128_desc_lo(ptx::smem_u32(sV), C::REGION_BYTES), 0), HI);
+        bool ok = true, issued_any = false;
+        int kq0 = 0, kq1 = 0;  // items of query tile 0 / 1 started so far
+        int cw0 = 0, cw1 = 0;  // score tiles of query tile 0 / 1 computed so far
+        int g = 0;             // key tiles consumed so far
+        for (int rnd = 0, it = blockIdx.x; ok && it < n_items; it = item_of_round(++rnd, blockIdx.x, gridDim.x)) {
+            const PackedWork x = make_work(p, it);
+            for (int u = -1; ok && u < x.T; ++u) {
+                if (u >= 0) {
+                    if (!ptx::mbar_wait_warp(&bar->v_full[(g + u) % NV], ((g + u) / NV) & 1, abort_flag)) { ok = false; break; }
+                }
+                bool k_ready = false;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int kq = i ? kq1 : kq0, cw = i ? cw1 : cw0;
+                    const int a = x.a[i], e = x.e[i];
+                    const uint32_t d_s = tm + C::tmem_s(i), d_o = tm + C::tmem_o(i);
+                    if (ok && u >= a && u < e) {
+                        // O_i += P_i(u) V(u), up to the last 16-key slice that a row of the tile sees
+                        const int c = u - a;
+                        if (c == 0 && kq > 0 && !ptx::mbar_wait_warp(&bar->o_empty[i], (kq - 1) & 1, abort_flag)) { ok = false; break; }
+                        if (!ptx::mbar_wait_warp(&bar->p_full[i], (cw + c) & 1, abort_flag)) { ok = false; break; }
+                        ptx::tc_fence_after();
+                        const uint64_t vb = v_d + ((g + u) % NV) * TILE16;
+                        const int seen = p.causal ? min(x.kv_len, x.pos0 + i * p.TT + x.tok[i]) : x.kv_len;
+                        const int slices = (seen - (x.J0 + u) * C::BN + 15) >> 4;
+#pragma unroll
+                        for (int kk = 0; kk < C::O_KSTEPS; ++kk)
+                            ptx::mma_ts_if(kk < slices ? issue : 0u, d_o, d_s + kk * 8,
+                                           vb + kk * ((C::O_ROWS * 128) >> 4), IDESC_O, (c > 0 || kk > 0) ? 1u : 0u);
+                        if (u == e - 1) ptx::mma_commit_if(issue, &bar->o_final[i]);
+                    }
+                    if (u + 1 >= a && u + 1 < e) {
+                        // S_i(u+1) = Q_i K(u+1)^T
+                        const int c = u + 1 - a;
+                        if (c == 0 && !ptx::mbar_wait_warp(&bar->q_loaded[i], kq & 1, abort_flag)) { ok = false; break; }
+                        if (!k_ready && !ptx::mbar_wait_warp(&bar->k_full[(g + u + 1) % NK], ((g + u + 1) / NK) & 1, abort_flag)) { ok = false; break; }
+                        k_ready = true;
+                        const uint64_t qa = q_d + i * TILE16, kb = k_d + ((g + u + 1) % NK) * TILE16;
+#pragma unroll
+                        for (int kk = 0; kk < C::S_KSTEPS; ++kk) {
+                            const uint64_t off = ((kk >> 2) * C::REGION_BYTES + (kk & 3) * 32) >> 4;
+                            ptx::mma_ss_if(issue, d_s, qa + off, kb + off, IDESC_S, kk > 0);
+                        }
+                        ptx::mma_commit_if(issue, &bar->s_full[i]);
+                        if (u + 1 == e - 1) ptx::mma_commit_if(issue, &bar->q_empty[i]);
+                        issued_any = true;
+                    }
+                }
+                if (!ok) break;
+                if (u >= 0) ptx::mma_commit_if(issue, &bar->v_empty[(g + u) % NV]);
+                if (u + 1 < x.T) ptx::mma_commit_if(issue, &bar->k_empty[(g + u + 1) % NK]);
+            }
+            if (x.e[0] > x.a[0]) { ++kq0; cw0 += x.e[0] - x.a[0]; }
+            if (x.e[1] > x.a[1]) { ++kq1; cw1 += x.e[1] - x.a[1]; }
+            g += x.T;
+        }
+        if (!ok) {
+            if (issue) {
+                *abort_flag = 1;
+                raise_status(kStatusTimeout);
+                if (issued_any) {
+                    ptx::mma_commit(&bar->drain);
+                    volatile int never = 0;
+                    ptx::mbar_wait(&bar->drain, 0, &never);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------ softmax warpgroups
+        const int wg = warp >> 2;
+        const int r = threadIdx.x & 127;
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lane_base + C::tmem_s(wg);
+        const uint32_t t_o = tmem + lane_base + C::tmem_o(wg);
+        const float sl = p.scale_log2;
+        const int my_tok = r / p.G, my_head = r - my_tok * p.G;  // this row's token in the tile and head in the group
+        bool ok = true;
+        int kq = 0, cw = 0;
+        int g = 0;  // key tiles of the items before
+        for (int rnd = 0, it = blockIdx.x; ok && it < n_items; it = item_of_round(++rnd, blockIdx.x, gridDim.x)) {
+            const PackedWork x = make_work(p, it);
+            const int n = wg ? x.e[1] - x.a[1] : x.e[0] - x.a[0];  // key tiles of this query tile
+            const int jb = x.J0 + (wg ? x.a[1] : x.a[0]);
+            const int tok = wg ? x.tok[1] : x.tok[0];
+            const bool live = my_tok < tok;  // tok <= TT: rows past G * TT never are
+            const int i_pos = x.pos0 + wg * p.TT + my_tok;
+            const int pos_first = x.pos0 + wg * p.TT;
+            float m_used = -INFINITY, l = 0.f;
+            for (int c = 0; ok && c < n; ++c) {
+                const int j0 = (jb + c) * C::BN;
+                if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->s_full[wg], (cw + c) & 1, abort_flag))) { ok = false; break; }
+                ptx::tc_fence_after();
+                uint32_t sv[C::BN];
+                ptx::tmem_ld128(t_s, sv);
+                float s[C::BN];
+#pragma unroll
+                for (int k = 0; k < C::BN; ++k) s[k] = __uint_as_float(sv[k]);
+                const bool need_mask = (j0 + C::BN > x.kv_len) || (p.causal && j0 + C::BN - 1 > pos_first) ||
+                                       (p.window > 0 && pos_first + tok - 1 - j0 >= p.window);
+                if (need_mask) {
+                    const int lo = p.window > 0 ? i_pos - p.window + 1 : 0;
+                    const int hi = live ? (p.causal ? i_pos : x.kv_len - 1) : -1;
+                    // columns lo - j0 .. hi - j0; the first bound may pass -2^31 for a huge window
+                    const int lo_c = p.window > i_pos ? 0 : lo - j0, hi_c = hi - j0;
+#pragma unroll
+                    for (int k = 0; k < C::BN; ++k)
+                        if (k < lo_c || k > hi_c) s[k] = -INFINITY;
+                }
+                float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]), mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
+#pragma unroll
+                for (int k = 8; k < C::BN; k += 8) {
+                    mx0 = ptx::fmax3(mx0, s[k], s[k + 1]);
+                    mx1 = ptx::fmax3(mx1, s[k + 2], s[k + 3]);
+                    mx2 = ptx::fmax3(mx2, s[k + 4], s[k + 5]);
+                    mx3 = ptx::fmax3(mx3, s[k + 6], s[k + 7]);
+                }
+                const float m_new = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl;
+                float alpha = 1.f;
+                bool rescale = false;
+                if (m_new > m_used + C::RESCALE_THRESHOLD) {
+                    alpha = ptx::ex2(m_used - m_new);
+                    m_used = m_new;
+                    rescale = true;
+                }
+                const float m_eff = (m_used == -INFINITY) ? 0.f : m_used;
+                const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(-m_eff, -m_eff);
+                float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0, acc2 = acc0, acc3 = acc0;
+                uint32_t pk[C::P_COLS];
+#pragma unroll
+                for (int k = 0; k < C::BN; k += 8) {
+                    float2 x0 = ptx::ffma2(make_float2(s[k], s[k + 1]), sl2, nm2);
+                    float2 x1 = ptx::ffma2(make_float2(s[k + 2], s[k + 3]), sl2, nm2);
+                    float2 x2 = ptx::ffma2(make_float2(s[k + 4], s[k + 5]), sl2, nm2);
+                    float2 x3 = ptx::ffma2(make_float2(s[k + 6], s[k + 7]), sl2, nm2);
+                    x0 = make_float2(ptx::ex2(x0.x), ptx::ex2(x0.y));
+                    x1 = make_float2(ptx::ex2(x1.x), ptx::ex2(x1.y));
+                    x2 = make_float2(ptx::ex2(x2.x), ptx::ex2(x2.y));
+                    // 1/8 of the exponentials on the FMA pipe, as in attn_fwd_kernel
+                    if ((k / 8) % 2 == 0)
+                        x3 = make_float2(ptx::ex2_poly(x3.x), ptx::ex2_poly(x3.y));
+                    else
+                        x3 = make_float2(ptx::ex2(x3.x), ptx::ex2(x3.y));
+                    acc0 = ptx::fadd2(acc0, x0);
+                    acc1 = ptx::fadd2(acc1, x1);
+                    acc2 = ptx::fadd2(acc2, x2);
+                    acc3 = ptx::fadd2(acc3, x3);
+                    pk[k / 2] = ptx::pack_bf16x2(x0.x, x0.y);
+                    pk[k / 2 + 1] = ptx::pack_bf16x2(x1.x, x1.y);
+                    pk[k / 2 + 2] = ptx::pack_bf16x2(x2.x, x2.y);
+                    pk[k / 2 + 3] = ptx::pack_bf16x2(x3.x, x3.y);
+                }
+                const float2 sum = ptx::fadd2(ptx::fadd2(acc0, acc1), ptx::fadd2(acc2, acc3));
+                l = l * alpha + (sum.x + sum.y);
+                ptx::tmem_st64(t_s, pk);
+                // the end of the sequence inside a 16-key slice: zero the slice's other V rows (both
+                // query tiles may do it: the same zeros, before either P is handed over)
+                const int tail = x.kv_len - j0;
+                if (tail < C::BN && (tail & 15)) {
+                    const int sv_st = (g + jb - x.J0 + c) % NV;
+                    if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->v_full[sv_st], ((g + jb - x.J0 + c) / NV) & 1, abort_flag))) { ok = false; break; }
+                    const uint32_t base = ptx::smem_u32(sV + sv_st * C::TILE_BYTES) + tail * 128;
+                    const int chunks = (16 - (tail & 15)) * 8;  // 16-byte pieces per region
+                    for (int t = r; t < chunks * C::NREG; t += 128)
+                        ptx::st_shared_v4(base + (t / chunks) * C::REGION_BYTES + (t % chunks) * 16, 0, 0, 0, 0);
+                    ptx::fence_proxy_async_smem();
+                }
+                if (c > 0 && __any_sync(0xffffffffu, rescale)) {
+                    const float2 al2 = make_float2(alpha, alpha);
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t v[32];
+                        ptx::tmem_ld32(t_o + cc * 32, v);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float2 y =
+                                ptx::fmul2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), al2);
+                            v[k] = __float_as_uint(y.x);
+                            v[k + 1] = __float_as_uint(y.y);
+                        }
+                        ptx::tmem_st32(t_o + cc * 32, v);
+                    }
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bar->p_full[wg]);
+            }
+            if (!ok) break;
+            g += x.T;
+            if (tok == 0) continue;
+            const size_t prow =
+                ((static_cast<size_t>(x.slot + x.part) * p.Hkv + x.g) * 256 + wg * 128 + r);  // partial-state row
+            if (n == 0) {
+                // an invalid length, or a part none of whose keys this query tile sees
+                if (x.kv_len < 0) {
+                    if (r == 0 && wg == 0 && x.g == 0) raise_status(kStatusBadSeqLen);
+                    if (live) {
+                        const size_t row = static_cast<size_t>(x.q_row + wg * p.TT + my_tok);
+                        const int h = x.g * p.G + my_head;
+                        uint4* dst = reinterpret_cast<uint4*>(p.o + (row * p.Hq + h) * D);
+                        for (int k = 0; k < D / 8; ++k)
+                            dst[k] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+                        if (p.lse != nullptr) p.lse[row * p.lse_t + h * p.lse_h] = __int_as_float(0x7fc00000);
+                    }
+                } else if (live) {
+                    p.ws_ml[prow * 2] = -INFINITY;
+                    p.ws_ml[prow * 2 + 1] = 0.f;
+                }
+                continue;
+            }
+            cw += n;
+            // ---- epilogue: O out of TMEM; normalised to the output, or as a partial state
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->o_final[wg], kq & 1, abort_flag))) { ok = false; break; }
+            ptx::tc_fence_after();
+            if (x.parts > 1) {
+#pragma unroll
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t v[32];
+                    ptx::tmem_ld32(t_o + cc * 32, v);
+                    if (live) {
+                        uint4* dst = reinterpret_cast<uint4*>(p.ws_o + prow * D + cc * 32);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    }
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bar->o_empty[wg]);
+                if (live) {
+                    p.ws_ml[prow * 2] = m_used;
+                    p.ws_ml[prow * 2 + 1] = l;
+                }
+            } else {
+                uint32_t w[D / 2];
+                const float inv_l = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t v[32];
+                    ptx::tmem_ld32(t_o + cc * 32, v);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        w[cc * 16 + k] =
+                            ptx::pack_bf16x2(__uint_as_float(v[2 * k]) * inv_l, __uint_as_float(v[2 * k + 1]) * inv_l);
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bar->o_empty[wg]);
+                if (live) {
+                    const size_t row = static_cast<size_t>(x.q_row + wg * p.TT + my_tok);
+                    const int h = x.g * p.G + my_head;
+                    uint4* dst = reinterpret_cast<uint4*>(p.o + (row * p.Hq + h) * D);
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    if (p.lse != nullptr)
+                        p.lse[row * p.lse_t + h * p.lse_h] = l > 0.f ? (m_used + ptx::lg2(l)) * kLn2 : -INFINITY;
+                }
+            }
+            ++kq;
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            raise_status(kStatusTimeout);
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// Joins the partial states of every block that was cut into parts, in ascending order: M = max m_i,
+// L = sum 2^(m_i - M) l_i, O = sum 2^(m_i - M) o_i / L, LSE = (M + log2 L) ln 2. One warp per row,
+// over all rows of all such blocks (none for most calls).
+template <int D>
+__global__ void __launch_bounds__(256) packed_merge_kernel(const PackedParams p, const SplitBlock* split) {
+    ptx::grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    constexpr int PER = D / 32;
+    const long long rows = static_cast<long long>(p.header->n_split) * p.Hkv * 256;
+    const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+    for (long long w = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); w < rows; w += warps) {
+        const int r = static_cast<int>(w & 255);
+        const long long bg = w >> 8;
+        const int g = static_cast<int>(bg % p.Hkv);
+        const SplitBlock b = split[bg / p.Hkv];
+        const int in_tile = (r & 127) / p.G;
+        const int tok = (r >> 7) * p.TT + in_tile;
+        if (in_tile >= p.TT || tok >= b.n_tok) continue;
+        const size_t step = static_cast<size_t>(p.Hkv) * 256;  // rows from one part's state to the next
+        const size_t row0 = (static_cast<size_t>(b.slot) * p.Hkv + g) * 256 + r;
+        float M = -INFINITY;
+        for (int i = lane; i < b.parts; i += 32) M = fmaxf(M, p.ws_ml[(row0 + i * step) * 2]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        float acc[PER], L = 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+        for (int i = 0; i < b.parts; ++i) {
+            const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + (row0 + i * step) * 2);
+            if (ml.x == -INFINITY) continue;  // the part holds none of the row's keys (and no output)
+            const float wt = ptx::ex2(ml.x - M);
+            L += wt * ml.y;
+            const float* oc = p.ws_o + (row0 + i * step) * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] += wt * oc[e];
+        }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const int h = g * p.G + (r & 127) - in_tile * p.G;
+        const size_t row = static_cast<size_t>(b.q_row) + tok;
+        __nv_bfloat16* orow = p.o + (row * p.Hq + h) * D + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; e += 2)
+            *reinterpret_cast<uint32_t*>(orow + e) = ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        if (p.lse != nullptr && lane == 0)
+            p.lse[row * p.lse_t + h * p.lse_h] = L > 0.f ? (M + ptx::lg2(L)) * kLn2 : -INFINITY;
+    }
+}
+
+}  // namespace attn

@@ -5,7 +5,11 @@
  * materialising the n x n score matrix in device memory:
  *   attn_fwd           prefill over whole sequences (causal / sliding-window / full, GQA, RoPE);
  *   attn_bwd           its gradients, recomputing the scores from the saved logsumexp;
- *   attn_decode_paged  one new query token per sequence over a paged KV cache.
+ *   attn_decode_paged  one new query token per sequence over a paged KV cache;
+ *   attn_packed_fwd, attn_packed_bwd   prefill and its gradients for sequences of different lengths,
+ *                      packed one behind the other without padding;
+ *   attn_chunk_paged   chunks of new tokens, of any length per sequence, over a paged KV cache;
+ *   attn_rope_axes     rotary positions with several axes on packed tokens.
  *
  * Conventions shared by every entry point:
  *   - Tensor arguments are plain device pointers to caller-owned memory, contiguous, in the
@@ -46,6 +50,7 @@ typedef enum {
 #define ATTN_DEVICE_TIMEOUT 1u      /* a pipeline wait exceeded its limit; that CTA bailed out */
 #define ATTN_DEVICE_BAD_PAGE 2u     /* a block-table entry outside [0, num_pages) was skipped */
 #define ATTN_DEVICE_BAD_SEQLEN 4u   /* a seq_len outside [1, max_blocks*page_size]; row set to NaN */
+#define ATTN_DEVICE_BAD_OFFSETS 8u  /* offsets of packed sequences that decrease or leave [0, T]; nothing computed */
 
 /*
  * attn_fwd -- attention forward (prefill), FlashAttention-style.
@@ -279,6 +284,134 @@ attn_status attn_decode_paged_noalloc(const void* q, const void* k_pages, const 
                                       const int32_t* block_table, const int32_t* seq_lens, int num_seqs,
                                       int max_blocks_per_seq, int num_pages, int page_size, int Hq, int Hkv, int D,
                                       float scale, void* o, float* lse, void* stream);
+
+/*
+ * Packed sequences. The entry points below take the tokens of num_seqs sequences one behind the other
+ * without padding: T rows [T, heads, D] (token-major), sequence s in rows [cu_seqlens[s],
+ * cu_seqlens[s+1]). Lengths may differ and may be zero. Shared by all of them:
+ *   cu_seqlens   int32 [num_seqs + 1] device, 0 <= cu_seqlens[0] <= ... <= cu_seqlens[num_seqs] <= T.
+ *          The host never reads it. Offsets that decrease or leave [0, T] set ATTN_DEVICE_BAD_OFFSETS
+ *          and nothing is computed. Rows of the outputs outside every sequence are left as they were,
+ *          and rows of the inputs there may hold anything (NaN included).
+ *   *_stride     elements from one token's row to the next (multiple of 8, >= heads * D): q, k and v
+ *          may be views of one projection's output. A token's heads are contiguous, 16-byte aligned.
+ *   T = 0        is valid: nothing is done.
+ *   workspace    device scratch of the size the *_workspace_size function gives for the call's sizes,
+ *          16-byte aligned, owned by the caller, any initial contents, overwritten; calls that overlap
+ *          on the GPU, and captured graphs that may run side by side, need their own.
+ * Within a sequence K and V must be finite. Values are bf16; scores, softmax statistics and sums are
+ * fp32, P is rounded to bf16 for its product as in attn_fwd. Constraints: D in {64, 128},
+ * Hq / Hkv <= 128 (else ATTN_ERR_UNSUPPORTED), (T + 128 * num_seqs) * Hq < 2^31. Nothing is allocated or
+ * cached, and the calls can be captured into a graph and replayed with other lengths.
+ */
+
+/*
+ * attn_packed_fwd_workspace_size -- bytes of workspace attn_packed_fwd needs: the list of work items
+ * and, for calls with few items, fp32 partial states of blocks whose keys are cut into parts (at most
+ * 592 / Hkv + 1 blocks of 256 rows per K/V head, D + 2 values each). 0 for invalid sizes.
+ */
+size_t attn_packed_fwd_workspace_size(int T, int num_seqs, int Hq, int Hkv, int D);
+
+/*
+ * attn_packed_fwd -- attn_fwd (without RoPE) for packed sequences: every sequence attends to itself
+ * ("attention-transformers", Q "How does self-attention work in a transformer?"), the masks counted
+ * from each sequence's own first token.
+ *   q      bf16 [T, Hq, D]; k, v bf16 [T, Hkv, D]; device, read only
+ *   o      bf16 [T, Hq, D] device, contiguous, written
+ *   lse    fp32 [Hq, T] device, written (natural log), or NULL
+ *   causal, window, scale   as attn_fwd
+ * Results depend on the lengths and values only and repeat bit for bit.
+ */
+attn_status attn_packed_fwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, const int32_t* cu_seqlens, int num_seqs, int T, int Hq, int Hkv, int D,
+                            int causal, int window, float scale, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * attn_packed_bwd_workspace_size -- bytes of workspace attn_packed_bwd needs: the tile list, and fp32
+ * (-LSE*log2 e, -D_i) and dq sums (D values) per query row padded to 128-row tiles of each sequence.
+ * 0 for invalid sizes.
+ */
+size_t attn_packed_bwd_workspace_size(int T, int num_seqs, int Hq, int D);
+
+/*
+ * attn_packed_bwd -- gradients of L = sum(O * dout) for attn_packed_fwd, with the formulas of attn_bwd.
+ *   q, k, v, strides, cu_seqlens, causal, window, scale   as given to attn_packed_fwd
+ *   o      bf16 [T, Hq, D] and lse fp32 [Hq, T]: attn_packed_fwd's outputs for these inputs
+ *   dout   bf16 [T, Hq, D] contiguous: gradient of the loss with respect to o, finite within sequences
+ *   dq     bf16 [T, Hq, D]; dk, dv bf16 [T, Hkv, D]: written, with strides of their own
+ * dk and dv repeat bit for bit; dq is a sum of fp32 partials (one per 128-key tile) added in the order
+ * the tiles finish, so for sequences of more than 256 tokens two calls may differ by one bf16 unit in
+ * the last place (a sum of at most two partials onto zero has one rounding whatever the order).
+ */
+attn_status attn_packed_bwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, const void* o, const float* lse, const void* dout, void* dq, void* dk,
+                            void* dv, int64_t dq_stride, int64_t dk_stride, int64_t dv_stride,
+                            const int32_t* cu_seqlens, int num_seqs, int T, int Hq, int Hkv, int D, int causal,
+                            int window, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_chunk_workspace_size -- bytes of workspace attn_chunk_paged needs, as
+ * attn_packed_fwd_workspace_size with sequences of up to max_blocks_per_seq * page_size keys.
+ */
+size_t attn_chunk_workspace_size(int T, int num_seqs, int max_blocks_per_seq, int page_size, int Hq, int Hkv, int D);
+
+/*
+ * attn_chunk_paged -- a serving step over the paged KV cache of attn_decode_paged in which every
+ * sequence brings its own number of new tokens: chunks of prompts, single decoded tokens, none at all.
+ * Sequence s brings n_s = cu_seqlens[s+1] - cu_seqlens[s] tokens, the last n_s of its seq_lens[s].
+ * 1. Append (when k_new is given): token t of sequence s is at position pos = seq_lens[s] - n_s + t; its
+ *    key and value go to page block_table[s][pos / 16], slot pos % 16 ("Self-Attention Complexity,
+ *    FlashAttention, PagedAttention, and RoPE in Code", Part 3: the cache grows one block-table slot at
+ *    a time). k_new == NULL: the cache already holds the new tokens.
+ * 2. Attend: each new token's queries attend to the cached tokens 0..pos (with window > 0: the last
+ *    `window` of them). Nothing is rotated: rotate q and k_new before (attn_rope_axes).
+ *   q            bf16 [T, Hq, D]; k_new, v_new bf16 [T, Hkv, D], or both NULL; device, read only
+ *   k_pages, v_pages, block_table   as attn_decode_paged; the new tokens' slots are written. Slots
+ *                written by two sequences in one call are the caller's error. page_size == 16.
+ *   seq_lens     int32 [num_seqs] device, each in [n_s, max_blocks_per_seq * 16] where n_s > 0 (not
+ *                read otherwise); else ATTN_DEVICE_BAD_SEQLEN is set, the sequence's rows of o and lse
+ *                are set to NaN and its tokens are not appended.
+ *   o            bf16 [T, Hq, D] device, contiguous, written; lse fp32 [T, Hq] device, written, or NULL
+ * A bad block-table entry sets ATTN_DEVICE_BAD_PAGE: its tokens are not appended and its keys and
+ * values are read as zeros (the output is then wrong). Slots past seq_lens may hold anything.
+ * Bad offsets: no output is written; tokens of sequences whose own two offsets are valid may be appended.
+ * With window > 0, pages that lie wholly before the window of the sequence's first new token are not
+ * read: their block-table entries may hold anything (a page that was given back, -1).
+ */
+attn_status attn_chunk_paged(const void* q, const void* k_new, const void* v_new, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, void* k_pages, void* v_pages, const int32_t* block_table,
+                             const int32_t* seq_lens, const int32_t* cu_seqlens, int num_seqs, int T,
+                             int max_blocks_per_seq, int num_pages, int page_size, int Hq, int Hkv, int D, int window,
+                             float scale, void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_rope_axes -- rotary positions with several axes (time, height, width of images and video), of
+ * the queries and keys of packed tokens ("attention-transformers", Q "How does Rotary Position
+ * Embedding (RoPE) work?", with a position per axis). The R/2 = sum(sections) first pairs of a head are
+ * rotated, each by the position of the axis it belongs to; the other D - R elements are copied.
+ *   q, q_out     bf16 [T, Hq, D]; k, k_out bf16 [T, Hk, D] (Hk = 0: no k, the pointers are not read);
+ *                device, token strides as above; out == in (same pointer and stride) rotates in place,
+ *                any other overlap is an error the call does not detect
+ *   positions    int32 [n_axes, T] device: any values (negative ones too)
+ *   sections     HOST array of n_axes (<= 8) pair counts, each >= 1; their sum a multiple of 8, <= D/2
+ *   interleave_axes  0: axis a owns sections[a] consecutive pairs, axis after axis; 1: pair i belongs to
+ *                axis i % n_axes while i < n_axes * sections[i % n_axes], else to axis 0 (every other
+ *                axis must find all its pairs that way)
+ *   per_axis_freq    0: pair i turns by theta_i = rope_base^(-i / (R/2)); 1: each axis has the
+ *                frequencies rope_base^(-j / sections[a]) for its j-th pair
+ *   rope_half_split  0: pairs (2i, 2i+1); 1: pairs (i, i + R/2)
+ *   rope_pos_scale   positions are divided by it (Position Interpolation); 1 = off
+ *   inverse      0: counter-clockwise by angle = position / rope_pos_scale * theta; 1: by -angle, which
+ *                is the rotation's gradient (from the gradients of the rotated q and k)
+ * The angle is formed in fp64 and reduced before sin and cos are taken in fp32; products are fp32,
+ * rounded once to bf16. D in {64, 128}, Hq, Hk <= 32767.
+ */
+attn_status attn_rope_axes(const void* q, void* q_out, const void* k, void* k_out, int64_t q_stride,
+                           int64_t q_out_stride, int64_t k_stride, int64_t k_out_stride, const int32_t* positions,
+                           int T, int Hq, int Hk, int D, int n_axes, const int* sections, int interleave_axes,
+                           int per_axis_freq, int rope_half_split, float rope_base, float rope_pos_scale, int inverse,
+                           void* stream);
 
 /*
  * attn_get_device_status -- synchronises `stream` on the current device, returns the device
