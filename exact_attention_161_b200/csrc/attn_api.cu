@@ -697,7 +697,7 @@ attn_status launch_packed(const PackedCall& c, cudaStream_t stream, int dev) {
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
     if ((st = ensure_smem(attn::attn_packed_kernel<D, kPaged>, C::SMEM_BYTES, dev)) != ATTN_OK) return st;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t lc = dependent_launch(grid, C::THREADS, C::SMEM_BYTES, stream, attr);
+    cudaLaunchConfig_t lc = dependent_launch(grid, attn::PackedCfg<D>::THREADS, C::SMEM_BYTES, stream, attr);
     CUDA_TRY(cudaLaunchKernelEx(&lc, attn::attn_packed_kernel<D, kPaged>, tq, tk, tv, p));
     if (L.max_slots > 0) {
         lc = dependent_launch(static_cast<unsigned>(2 * sms), 256, 0, stream, attr);

@@ -316,33 +316,35 @@ struct PackedParams {
     int debug_drop_copy;         // test hook: CTA 0 skips its first key-tile copy (see attn.h)
 };
 
-// An item of the list for one K/V head, with the key-tile range of each of its two query tiles.
-struct PackedWork {
-    int q_row, pos0, kv, kv_len, n_tok, part, parts, slot, g;
+// An item of the list for one K/V head, with the key-tile range of each of its two query tiles. The
+// producer decodes the items into a small ring in shared memory, ahead of the other warps: the record's
+// load and the arithmetic are then off the path from one item's last product to the next one's first.
+struct alignas(16) PackedWork {
+    int q_row, pos0, kv, kv_len;
     int J0, T;          // key tiles of the item
+    int g, parts;       // K/V head; parts of the block
     int tok[2];         // tokens of query tile i (0: absent)
+    int state;          // partial-state slot (blocks of more than one part)
+    int pad;
     int a[2], e[2];     // visible key tiles of query tile i: [J0 + a, J0 + e)
 };
 
-__device__ __forceinline__ PackedWork make_work(const PackedParams& p, int it) {
+__device__ __forceinline__ PackedWork decode_item(const PackedParams& p, const int4& lo, const int4& hi, int g) {
     PackedWork w;
-    const int entry = it / p.Hkv;
-    w.g = it - entry * p.Hkv;
-    const int4* rec = reinterpret_cast<const int4*>(p.items + entry);
-    const int4 lo = rec[0], hi = rec[1];
+    w.g = g;
     w.q_row = lo.x;
     w.pos0 = lo.y;
     w.kv = lo.z;
     w.kv_len = lo.w;
     w.J0 = hi.x;
     w.T = hi.y;
-    w.n_tok = hi.z & 1023;
-    w.part = (hi.z >> 10) & 1023;
+    const int n_tok = hi.z & 1023;
     w.parts = ((hi.z >> 20) & 1023) + 1;
-    w.slot = hi.w;
+    w.state = hi.w + ((hi.z >> 10) & 1023);
+    w.pad = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int n = min(p.TT, w.n_tok - i * p.TT);
+        const int n = min(p.TT, n_tok - i * p.TT);
         w.tok[i] = max(0, n);
         w.a[i] = w.e[i] = 0;
         if (n > 0 && w.T > 0) {
@@ -358,19 +360,52 @@ __device__ __forceinline__ PackedWork make_work(const PackedParams& p, int it) {
     return w;
 }
 
+constexpr int kWorkRing = 4;
+
+template <int NK, int NV>
+struct PackedBarriers : FwdBarriers<NK, NV> {
+    uint64_t work_full[kWorkRing], work_empty[kWorkRing];
+    uint64_t s_free[2], pv_done[2], drain_outputs;  // kSplitP
+    PackedWork work[kWorkRing];
+};
+
+// Sets the columns of s outside [lo, hi] to -inf: a bit per column, 32 columns at a time (two
+// instructions per score, where two compares and a select are three).
+template <int N>
+__device__ __forceinline__ void mask_columns(float (&s)[N], int lo, int hi) {
+    auto low_bits = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+#pragma unroll
+    for (int w = 0; w < N / 32; ++w) {
+        const uint32_t m = low_bits(hi + 1 - 32 * w) & ~low_bits(lo - 32 * w);
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if (!((m >> k) & 1u)) s[32 * w + k] = -INFINITY;
+    }
+}
+
+template <int D>
+struct PackedCfg {
+    static constexpr bool kSplitP = D == 64;
+    static constexpr int THREADS = FwdCfg<D>::THREADS + (kSplitP ? 32 : 0);  // a second MMA issuer
+};
+
 template <int D, bool kPaged>
-__global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
+__global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
     attn_packed_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PackedParams p) {
     using C = FwdCfg<D>;
     constexpr int NK = C::NK, NV = C::NV;
     constexpr int kPages = C::BN / kPageSize;  // pages of a key tile
+    // At D = 64 Tensor Memory has room for P beside S: see the MMA issuer.
+    constexpr bool kSplitP = PackedCfg<D>::kSplitP;
+    constexpr int kConsumers = kSplitP ? 10 : 9;  // warps that read the work ring: softmax and MMA issuers
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
     uint8_t* sK = sQ + C::QT * C::TILE_BYTES;
     uint8_t* sV = sK + NK * C::TILE_BYTES;
-    auto* bar = reinterpret_cast<FwdBarriers<NK, NV>*>(sV + NV * C::TILE_BYTES);
+    auto* bar = reinterpret_cast<PackedBarriers<NK, NV>*>(sV + NV * C::TILE_BYTES);
+    static_assert(sizeof(PackedBarriers<NK, NV>) <= 1024, "barrier block larger than its reserved bytes");
     volatile int* abort_flag = &bar->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -382,6 +417,12 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
             ptx::mbar_init(&bar->p_full[i], 128);
             ptx::mbar_init(&bar->o_final[i], 1);
             ptx::mbar_init(&bar->o_empty[i], 128);
+            ptx::mbar_init(&bar->s_free[i], 128);
+            ptx::mbar_init(&bar->pv_done[i], 1);
+        }
+        for (int s = 0; s < kWorkRing; ++s) {
+            ptx::mbar_init(&bar->work_full[s], 1);
+            ptx::mbar_init(&bar->work_empty[s], kConsumers);
         }
         for (int s = 0; s < NK; ++s) {
             ptx::mbar_init(&bar->k_full[s], 1);
@@ -392,6 +433,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
             ptx::mbar_init(&bar->v_empty[s], 1);
         }
         ptx::mbar_init(&bar->drain, 1);
+        ptx::mbar_init(&bar->drain_outputs, 1);
         bar->abort = 0;
         ptx::fence_mbar_init();
     }
@@ -411,6 +453,8 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = bar->tmem_base;
     const int n_items = p.header->n_items * p.Hkv;
+    // TMEM columns of P: over the first half of S, or behind the accumulators
+    auto tmem_p = [](int i) { return kSplitP ? 256u + 2u * D + 64u * i : C::tmem_s(i); };
 
     if (warp == C::PRODUCER_WARP) {
         // ------------------------------------------------------------------ TMA producer
@@ -419,8 +463,24 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         int kq[2] = {0, 0};
         int g = 0, k_issued = 0, v_issued = 0;
         bool ok = true;
-        for (int rnd = 0, it = blockIdx.x; ok && it < n_items; it = item_of_round(++rnd, blockIdx.x, gridDim.x)) {
-            const PackedWork x = make_work(p, it);
+        int4 rec_lo{}, rec_hi{};  // the next item's record, loaded one item ahead
+        auto load_record = [&](int it) {
+            if (it >= n_items) return;
+            const int4* rec = reinterpret_cast<const int4*>(p.items + it / p.Hkv);
+            rec_lo = rec[0];
+            rec_hi = rec[1];
+        };
+        load_record(blockIdx.x);
+        for (int rnd = 0, it = blockIdx.x, next; ok && it < n_items; it = next) {
+            const PackedWork x = decode_item(p, rec_lo, rec_hi, it % p.Hkv);
+            const int ws = rnd % kWorkRing;
+            if (rnd >= kWorkRing && !ptx::mbar_wait_warp(&bar->work_empty[ws], (rnd / kWorkRing - 1) & 1, abort_flag)) { ok = false; break; }
+            if (lane == 0) {
+                bar->work[ws] = x;
+                ptx::mbar_arrive(&bar->work_full[ws]);
+            }
+            next = item_of_round(++rnd, blockIdx.x, gridDim.x);
+            load_record(next);
             for (int i = 0; i < 2 && ok; ++i) {
                 if (x.e[i] == x.a[i]) continue;
                 if (kq[i] > 0 && !ptx::mbar_wait_warp(&bar->q_empty[i], (kq[i] - 1) & 1, abort_flag)) { ok = false; break; }
@@ -507,8 +567,14 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
             for (int u = max(0, v_issued - NV); u < v_issued; ++u) ptx::mbar_wait(&bar->v_full[u % NV], (u / NV) & 1, &never);
         }
         __syncwarp();
-    } else if (warp == C::MMA_WARP) {
-        // ------------------------------------------------------------------ MMA issuer
+    } else if (warp >= C::MMA_WARP) {
+        // ------------------------------------------------------------------ MMA issuers
+        // With P over S (D = 128) one warp issues, per key tile u: O_i += P_i(u) V(u), S_i(u+1) = Q_i K(u+1)^T
+        // for i = 0, 1, in execution order. With P in columns of its own (D = 64) S_i(u + 1) only waits
+        // until the softmax has read S_i(u), and a second warp issues the outputs: the scores run ahead,
+        // across the items too. What a warp issues between two products counts (the softmax warps take most
+        // issue slots): stages and parities are stepped, not computed.
+        const bool scores = warp == C::MMA_WARP, outputs = !kSplitP || !scores;
         const uint32_t issue = ptx::elect_one() ? 1u : 0u;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, C::BN, 0, 0);
@@ -520,69 +586,113 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         const uint64_t v_d =
             ptx::desc64(__shfl_sync(0xffffffffu, ptx::sw128_desc_lo(ptx::smem_u32(sV), C::REGION_BYTES), 0), HI);
         bool ok = true, issued_any = false;
-        int kq0 = 0, kq1 = 0;  // items of query tile 0 / 1 started so far
-        int cw0 = 0, cw1 = 0;  // score tiles of query tile 0 / 1 computed so far
-        int g = 0;             // key tiles consumed so far
+        int sk = 0, sv = 0;            // ring stages of the next K and V tile
+        uint32_t pk = 0, pv = 0;       // and their parities
+        uint32_t q_par[2] = {0, 0}, p_par[2] = {0, 0}, o_par[2] = {1, 1}, f_par[2] = {1, 1};
+        int a[2], e[2], seen[2];       // of the current item: visible key tiles, keys the tile's last row sees
+        auto score_tile = [&](int i, bool first, bool last) {
+            if (first) {
+                if (!ptx::mbar_wait_warp(&bar->q_loaded[i], q_par[i], abort_flag)) return false;
+                q_par[i] ^= 1;
+            }
+            if (kSplitP) {  // the softmax has read the scores before (a fresh barrier passes parity 1)
+                if (!ptx::mbar_wait_warp(&bar->s_free[i], f_par[i], abort_flag)) return false;
+                f_par[i] ^= 1;
+                ptx::tc_fence_after();
+            }
+            const uint64_t qa = q_d + i * TILE16, kb = k_d + sk * TILE16;
+#pragma unroll
+            for (int kk = 0; kk < C::S_KSTEPS; ++kk) {
+                const uint64_t off = ((kk >> 2) * C::REGION_BYTES + (kk & 3) * 32) >> 4;
+                ptx::mma_ss_if(issue, tm + C::tmem_s(i), qa + off, kb + off, IDESC_S, kk > 0);
+            }
+            ptx::mma_commit_if(issue, &bar->s_full[i]);
+            if (last) ptx::mma_commit_if(issue, &bar->q_empty[i]);
+            issued_any = true;
+            return true;
+        };
+        // up to the last 16-key slice that a row of the tile sees; keys: how many from the tile's first key on
+        auto output_tile = [&](int i, bool first, bool last, int keys) {
+            if (first) {  // the epilogue before has read O (a fresh barrier passes parity 1)
+                if (!ptx::mbar_wait_warp(&bar->o_empty[i], o_par[i], abort_flag)) return false;
+                o_par[i] ^= 1;
+            }
+            if (!ptx::mbar_wait_warp(&bar->p_full[i], p_par[i], abort_flag)) return false;
+            p_par[i] ^= 1;
+            ptx::tc_fence_after();
+            const uint32_t d_o = tm + C::tmem_o(i), d_p = tm + tmem_p(i);
+            const uint64_t vb = v_d + sv * TILE16;
+            const uint32_t acc = first ? 0u : 1u;
+            if (keys > 112) {
+#pragma unroll
+                for (int kk = 0; kk < C::O_KSTEPS; ++kk)
+                    ptx::mma_ts_if(issue, d_o, d_p + kk * 8, vb + kk * ((C::O_ROWS * 128) >> 4), IDESC_O, kk > 0 ? 1u : acc);
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < C::O_KSTEPS - 1; ++kk)
+                    ptx::mma_ts_if(kk * 16 < keys ? issue : 0u, d_o, d_p + kk * 8, vb + kk * ((C::O_ROWS * 128) >> 4), IDESC_O,
+                                   kk > 0 ? 1u : acc);
+            }
+            if (kSplitP)
+                ptx::mma_commit_if(issue, &bar->pv_done[i]);
+            else if (last)
+                ptx::mma_commit_if(issue, &bar->o_final[i]);
+            issued_any = true;
+            return true;
+        };
         for (int rnd = 0, it = blockIdx.x; ok && it < n_items; it = item_of_round(++rnd, blockIdx.x, gridDim.x)) {
-            const PackedWork x = make_work(p, it);
-            for (int u = -1; ok && u < x.T; ++u) {
-                if (u >= 0) {
-                    if (!ptx::mbar_wait_warp(&bar->v_full[(g + u) % NV], ((g + u) / NV) & 1, abort_flag)) { ok = false; break; }
+            const int ws = rnd % kWorkRing;
+            if (!ptx::mbar_wait_warp(&bar->work_full[ws], (rnd / kWorkRing) & 1, abort_flag)) { ok = false; break; }
+            const PackedWork& x = bar->work[ws];
+            const int T = x.T, key0 = x.J0 * C::BN;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                a[i] = x.a[i];
+                e[i] = x.e[i];
+                seen[i] = (p.causal ? min(x.kv_len, x.pos0 + i * p.TT + x.tok[i]) : x.kv_len) - key0;
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bar->work_empty[ws]);
+            for (int u = kSplitP ? 0 : -1; ok && u < T; ++u) {
+                const int us = kSplitP ? u : u + 1;  // the key tile whose scores this step computes
+                if (outputs && u >= 0) {
+                    if (!ptx::mbar_wait_warp(&bar->v_full[sv], pv, abort_flag)) { ok = false; break; }
                 }
-                bool k_ready = false;
+                if (scores && us < T) {
+                    if (!ptx::mbar_wait_warp(&bar->k_full[sk], pk, abort_flag)) { ok = false; break; }
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int kq = i ? kq1 : kq0, cw = i ? cw1 : cw0;
-                    const int a = x.a[i], e = x.e[i];
-                    const uint32_t d_s = tm + C::tmem_s(i), d_o = tm + C::tmem_o(i);
-                    if (ok && u >= a && u < e) {
-                        // O_i += P_i(u) V(u), up to the last 16-key slice that a row of the tile sees
-                        const int c = u - a;
-                        if (c == 0 && kq > 0 && !ptx::mbar_wait_warp(&bar->o_empty[i], (kq - 1) & 1, abort_flag)) { ok = false; break; }
-                        if (!ptx::mbar_wait_warp(&bar->p_full[i], (cw + c) & 1, abort_flag)) { ok = false; break; }
-                        ptx::tc_fence_after();
-                        const uint64_t vb = v_d + ((g + u) % NV) * TILE16;
-                        const int seen = p.causal ? min(x.kv_len, x.pos0 + i * p.TT + x.tok[i]) : x.kv_len;
-                        const int slices = (seen - (x.J0 + u) * C::BN + 15) >> 4;
-#pragma unroll
-                        for (int kk = 0; kk < C::O_KSTEPS; ++kk)
-                            ptx::mma_ts_if(kk < slices ? issue : 0u, d_o, d_s + kk * 8,
-                                           vb + kk * ((C::O_ROWS * 128) >> 4), IDESC_O, (c > 0 || kk > 0) ? 1u : 0u);
-                        if (u == e - 1) ptx::mma_commit_if(issue, &bar->o_final[i]);
-                    }
-                    if (u + 1 >= a && u + 1 < e) {
-                        // S_i(u+1) = Q_i K(u+1)^T
-                        const int c = u + 1 - a;
-                        if (c == 0 && !ptx::mbar_wait_warp(&bar->q_loaded[i], kq & 1, abort_flag)) { ok = false; break; }
-                        if (!k_ready && !ptx::mbar_wait_warp(&bar->k_full[(g + u + 1) % NK], ((g + u + 1) / NK) & 1, abort_flag)) { ok = false; break; }
-                        k_ready = true;
-                        const uint64_t qa = q_d + i * TILE16, kb = k_d + ((g + u + 1) % NK) * TILE16;
-#pragma unroll
-                        for (int kk = 0; kk < C::S_KSTEPS; ++kk) {
-                            const uint64_t off = ((kk >> 2) * C::REGION_BYTES + (kk & 3) * 32) >> 4;
-                            ptx::mma_ss_if(issue, d_s, qa + off, kb + off, IDESC_S, kk > 0);
-                        }
-                        ptx::mma_commit_if(issue, &bar->s_full[i]);
-                        if (u + 1 == e - 1) ptx::mma_commit_if(issue, &bar->q_empty[i]);
-                        issued_any = true;
-                    }
+                    if (outputs && ok && u >= a[i] && u < e[i])
+                        ok = output_tile(i, u == a[i], u == e[i] - 1, seen[i] - u * C::BN);
+                    if (scores && ok && us >= a[i] && us < e[i]) ok = score_tile(i, us == a[i], us == e[i] - 1);
                 }
                 if (!ok) break;
-                if (u >= 0) ptx::mma_commit_if(issue, &bar->v_empty[(g + u) % NV]);
-                if (u + 1 < x.T) ptx::mma_commit_if(issue, &bar->k_empty[(g + u + 1) % NK]);
+                if (outputs && u >= 0) {
+                    ptx::mma_commit_if(issue, &bar->v_empty[sv]);
+                    if (++sv == NV) {
+                        sv = 0;
+                        pv ^= 1;
+                    }
+                }
+                if (scores && us < T) {
+                    ptx::mma_commit_if(issue, &bar->k_empty[sk]);
+                    if (++sk == NK) {
+                        sk = 0;
+                        pk ^= 1;
+                    }
+                }
             }
-            if (x.e[0] > x.a[0]) { ++kq0; cw0 += x.e[0] - x.a[0]; }
-            if (x.e[1] > x.a[1]) { ++kq1; cw1 += x.e[1] - x.a[1]; }
-            g += x.T;
         }
         if (!ok) {
             if (issue) {
                 *abort_flag = 1;
                 raise_status(kStatusTimeout);
                 if (issued_any) {
-                    ptx::mma_commit(&bar->drain);
+                    uint64_t* drain = scores ? &bar->drain : &bar->drain_outputs;
+                    ptx::mma_commit(drain);
                     volatile int never = 0;
-                    ptx::mbar_wait(&bar->drain, 0, &never);
+                    ptx::mbar_wait(drain, 0, &never);
                 }
             }
         }
@@ -593,14 +703,20 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
         const int r = threadIdx.x & 127;
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lane_base + C::tmem_s(wg);
-        const uint32_t t_o = tmem + lane_base + C::tmem_o(wg);
+        const uint32_t t_o = tmem + lane_base + C::tmem_o(wg), t_p = tmem + lane_base + tmem_p(wg);
         const float sl = p.scale_log2;
         const int my_tok = r / p.G, my_head = r - my_tok * p.G;  // this row's token in the tile and head in the group
         bool ok = true;
         int kq = 0, cw = 0;
         int g = 0;  // key tiles of the items before
         for (int rnd = 0, it = blockIdx.x; ok && it < n_items; it = item_of_round(++rnd, blockIdx.x, gridDim.x)) {
-            const PackedWork x = make_work(p, it);
+            const int ws = rnd % kWorkRing;
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->work_full[ws], (rnd / kWorkRing) & 1, abort_flag))) { ok = false; break; }
+            const PackedWork& x = bar->work[ws];  // kept until the item is done: registers are scarce here
+            auto release_work = [&]() {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bar->work_empty[ws]);
+            };
             const int n = wg ? x.e[1] - x.a[1] : x.e[0] - x.a[0];  // key tiles of this query tile
             const int jb = x.J0 + (wg ? x.a[1] : x.a[0]);
             const int tok = wg ? x.tok[1] : x.tok[0];
@@ -614,6 +730,10 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
                 ptx::tc_fence_after();
                 uint32_t sv[C::BN];
                 ptx::tmem_ld128(t_s, sv);
+                if constexpr (kSplitP) {
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&bar->s_free[wg]);
+                }
                 float s[C::BN];
 #pragma unroll
                 for (int k = 0; k < C::BN; ++k) s[k] = __uint_as_float(sv[k]);
@@ -624,9 +744,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
                     const int hi = live ? (p.causal ? i_pos : x.kv_len - 1) : -1;
                     // columns lo - j0 .. hi - j0; the first bound may pass -2^31 for a huge window
                     const int lo_c = p.window > i_pos ? 0 : lo - j0, hi_c = hi - j0;
-#pragma unroll
-                    for (int k = 0; k < C::BN; ++k)
-                        if (k < lo_c || k > hi_c) s[k] = -INFINITY;
+                    mask_columns(s, lo_c, hi_c);
                 }
                 float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]), mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
 #pragma unroll
@@ -659,7 +777,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
                     x2 = make_float2(ptx::ex2(x2.x), ptx::ex2(x2.y));
                     // 1/8 of the exponentials on the FMA pipe, as in attn_fwd_kernel
                     if ((k / 8) % 2 == 0)
-                        x3 = make_float2(ptx::ex2_poly(x3.x), ptx::ex2_poly(x3.y));
+                        x3 = make_float2(ptx::ex2_poly4(x3.x), ptx::ex2_poly4(x3.y));
                     else
                         x3 = make_float2(ptx::ex2(x3.x), ptx::ex2(x3.y));
                     acc0 = ptx::fadd2(acc0, x0);
@@ -673,7 +791,12 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
                 }
                 const float2 sum = ptx::fadd2(ptx::fadd2(acc0, acc1), ptx::fadd2(acc2, acc3));
                 l = l * alpha + (sum.x + sum.y);
-                ptx::tmem_st64(t_s, pk);
+                if constexpr (kSplitP) {
+                    // P and O are free once the product before has completed
+                    if (cw + c > 0 && !__all_sync(0xffffffffu, ptx::mbar_wait(&bar->pv_done[wg], (cw + c - 1) & 1, abort_flag))) { ok = false; break; }
+                    ptx::tc_fence_after();
+                }
+                ptx::tmem_st64(t_p, pk);
                 // the end of the sequence inside a 16-key slice: zero the slice's other V rows (both
                 // query tiles may do it: the same zeros, before either P is handed over)
                 const int tail = x.kv_len - j0;
@@ -707,9 +830,12 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
             }
             if (!ok) break;
             g += x.T;
-            if (tok == 0) continue;
+            if (tok == 0) {
+                release_work();
+                continue;
+            }
             const size_t prow =
-                ((static_cast<size_t>(x.slot + x.part) * p.Hkv + x.g) * 256 + wg * 128 + r);  // partial-state row
+                ((static_cast<size_t>(x.state) * p.Hkv + x.g) * 256 + wg * 128 + r);  // partial-state row
             if (n == 0) {
                 // an invalid length, or a part none of whose keys this query tile sees
                 if (x.kv_len < 0) {
@@ -726,11 +852,13 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
                     p.ws_ml[prow * 2] = -INFINITY;
                     p.ws_ml[prow * 2 + 1] = 0.f;
                 }
+                release_work();
                 continue;
             }
             cw += n;
             // ---- epilogue: O out of TMEM; normalised to the output, or as a partial state
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->o_final[wg], kq & 1, abort_flag))) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, kSplitP ? ptx::mbar_wait(&bar->pv_done[wg], (cw - 1) & 1, abort_flag)
+                                                 : ptx::mbar_wait(&bar->o_final[wg], kq & 1, abort_flag))) { ok = false; break; }
             ptx::tc_fence_after();
             if (x.parts > 1) {
 #pragma unroll
@@ -738,9 +866,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
                     uint32_t v[32];
                     ptx::tmem_ld32(t_o + cc * 32, v);
                     if (live) {
-                        uint4* dst = reinterpret_cast<uint4*>(p.ws_o + prow * D + cc * 32);
+                        uint32_t* dst = reinterpret_cast<uint32_t*>(p.ws_o + prow * D + cc * 32);  // 256-byte aligned rows
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        for (int k = 0; k < 32; k += 8) ptx::st_global_v8(dst + k, v + k);
                     }
                 }
                 ptx::tc_fence_before();
@@ -766,14 +894,22 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
                 if (live) {
                     const size_t row = static_cast<size_t>(x.q_row + wg * p.TT + my_tok);
                     const int h = x.g * p.G + my_head;
-                    uint4* dst = reinterpret_cast<uint4*>(p.o + (row * p.Hq + h) * D);
+                    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row * p.Hq + h) * D);
+                    // whole 32-byte sectors where the tensor's alignment allows it
+                    if ((reinterpret_cast<uintptr_t>(p.o) & 31) == 0) {
 #pragma unroll
-                    for (int k = 0; k < D / 8; ++k) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                        for (int k = 0; k < D / 2; k += 8) ptx::st_global_v8(dst + k, w + k);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < D / 2; k += 4)
+                            *reinterpret_cast<uint4*>(dst + k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+                    }
                     if (p.lse != nullptr)
                         p.lse[row * p.lse_t + h * p.lse_h] = l > 0.f ? (m_used + ptx::lg2(l)) * kLn2 : -INFINITY;
                 }
             }
             ++kq;
+            release_work();
         }
         if (!ok) {
             *abort_flag = 1;

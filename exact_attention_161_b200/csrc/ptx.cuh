@@ -437,11 +437,30 @@ __device__ __forceinline__ float2 ex2_poly2(float2 x) {
                        __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
 }
 
+// As ex2_poly with a degree-4 polynomial from the same fit: largest relative error 2.9e-06, where the
+// sum of the probabilities has to keep more than bf16's bits (logsumexp over few keys).
+__device__ __forceinline__ float ex2_poly4(float x) {
+    x = fmaxf(x, -127.f);
+    const float t = x + 12582912.f;  // as in ex2_poly
+    const float f = x - (t - 12582912.f);
+    float q = fmaf(0x1.3a02a8p-7f, f, 0x1.c9fc4p-5f);
+    q = fmaf(q, f, 0x1.ec0378p-3f);
+    q = fmaf(q, f, 0x1.62e12cp-1f);
+    q = fmaf(q, f, 1.f);
+    return __int_as_float(__float_as_int(q) + (__float_as_int(t) << 23));
+}
+
 // max(a, b, c) in one instruction (sm_100a).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+// 32 bytes to a 32-byte aligned global address (sm_100a).
+__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 // Two fp32 -> packed bf16x2 (round to nearest even); lo goes to the low half.
 // Four fp32 values to e4m3 (nearest even, saturating at +-448), byte i = value i.
