@@ -297,47 +297,54 @@ def attn_decode_paged_noalloc(q, k_pages, v_pages, block_table, seq_lens, scale=
     return o, lse
 
 
-def _token_rows(t, name):
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _ptr(t, name, dtype, dev):
+    """Address of a contiguous tensor of the given type on CUDA device `dev` (an index)."""
+    if t.get_device() != dev:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _rows(t, name, dev):
     """A bf16 tensor [T, heads, D] whose tokens hold their heads one behind the other, any distance
-    apart (a view of a fused projection's output is one): its pointer and token stride."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype != torch.bfloat16:
-        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    apart (a view of a fused projection's output is one): its address and token stride."""
+    if t.get_device() != dev:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, dev, t.device))
+    if t.dtype != _BF16:
+        raise TypeError("%s must be %s, got %s" % (name, _BF16, t.dtype))
     T, H, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if T > 1 else H * D
+    return t.data_ptr(), st if T > 1 else H * D
 
 
-class _Launch:
-    """Makes the device of the call's tensors current and the given stream torch's stream, so that
-    what the call allocates belongs to the stream it runs on."""
+def _device_of(q):
+    dev = q.get_device()
+    if dev < 0:
+        raise TypeError("q must be a CUDA tensor")
+    return dev
 
-    def __init__(self, stream, first, *others):
-        for t in others:
-            if t is not None and t.device != first.device:
-                raise ValueError("tensors of one call must be on one device, got %s and %s" % (first.device, t.device))
-        if first.device.type != "cuda":
-            raise TypeError("q must be a CUDA tensor")
-        self.device, self.guards = first.device, []
-        if first.device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(first.device))
-        self.given = stream
 
-    def __enter__(self):
-        if self.given is not None:
-            s = self.given
-            if not isinstance(s, torch.cuda.Stream):
-                s = torch.cuda.ExternalStream(int(getattr(s, "cuda_stream", s)), device=self.device)
-            self.guards.append(torch.cuda.stream(s))
-        for g in self.guards:
-            g.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _on(dev, stream, call):
+    """call(raw stream) with `dev` the current device and the given stream (a torch stream or an address)
+    torch's current one, so that what the call allocates belongs to the stream it runs on."""
+    if stream is None and dev == _current_device():
+        return call(_raw_stream(dev))
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call(_raw_stream(dev))
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=dev)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _check_packed_shapes(q, k, v, cu_seqlens):
@@ -345,11 +352,6 @@ def _check_packed_shapes(q, k, v, cu_seqlens):
         raise ValueError("q must be [T, Hq, D], k and v [T, Hkv, D]")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be [num_seqs + 1]")
-
-
-def _workspace(given, need, device):
-    ws = torch.empty(need, dtype=torch.uint8, device=device) if given is None else given
-    return _dev_tensor(ws, "workspace", torch.uint8), ws.numel(), ws
 
 
 def packed_fwd_workspace_size(T, num_seqs, Hq, Hkv, D) -> int:
@@ -364,22 +366,24 @@ def attn_packed_fwd(q, k, v, cu_seqlens, causal=False, window=0, scale=0.0, o=No
     bf16, lse [Hq,T] fp32 or None); rows outside every sequence are not written."""
     _check_packed_shapes(q, k, v, cu_seqlens)
     T, Hq, D = q.shape
-    Hkv, S = k.shape[1], cu_seqlens.numel() - 1
+    Hkv, S, dev = k.shape[1], cu_seqlens.shape[0] - 1, _device_of(q)
     if o is not None and o.shape != q.shape or lse is not None and lse.shape != (Hq, T):
         raise ValueError("o must be [T, Hq, D] and lse [Hq, T]")
-    with _Launch(stream, q, k, v, cu_seqlens, o, lse, workspace) as st:
-        if o is None:
-            o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-        if lse is None and want_lse:
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-        (qp, qs), (kp, ks), (vp, vs) = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
-        ws, ws_bytes, _keep = _workspace(workspace, packed_fwd_workspace_size(T, S, Hq, Hkv, D), q.device)
-        _check(lib.attn_packed_fwd(qp, kp, vp, qs, ks, vs, _dev_tensor(cu_seqlens, "cu_seqlens", torch.int32), S, T, Hq,
-                                   Hkv, D, int(bool(causal)), int(window), float(scale),
-                                   _dev_tensor(o, "o", torch.bfloat16),
-                                   _dev_tensor(lse, "lse", torch.float32) if lse is not None else None, ws, ws_bytes,
-                                   st))
-    return o, lse
+
+    def call(st):
+        out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device) if o is None else o
+        stats = torch.empty((Hq, T), dtype=_F32, device=q.device) if lse is None and want_lse else lse
+        (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", dev), _rows(k, "k", dev), _rows(v, "v", dev)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(lib.attn_packed_fwd_workspace_size(T, S, Hq, Hkv, D), dtype=_U8, device=q.device)
+        _check(lib.attn_packed_fwd(qp, kp, vp, qs, ks, vs, _ptr(cu_seqlens, "cu_seqlens", _I32, dev), S, T, Hq, Hkv, D,
+                                   bool(causal), window, scale, _ptr(out, "o", _BF16, dev),
+                                   None if stats is None else _ptr(stats, "lse", _F32, dev),
+                                   _ptr(ws, "workspace", _U8, dev), ws.numel(), st))
+        return out, stats
+
+    return _on(dev, stream, call)
 
 
 def packed_bwd_workspace_size(T, num_seqs, Hq, D) -> int:
@@ -393,23 +397,28 @@ def attn_packed_bwd(q, k, v, o, lse, dout, cu_seqlens, causal=False, window=0, s
     token strides of their own. Rows outside every sequence are not written."""
     _check_packed_shapes(q, k, v, cu_seqlens)
     T, Hq, D = q.shape
-    Hkv, S = k.shape[1], cu_seqlens.numel() - 1
+    Hkv, S, dev = k.shape[1], cu_seqlens.shape[0] - 1, _device_of(q)
     if o.shape != q.shape or dout.shape != q.shape or lse.shape != (Hq, T):
         raise ValueError("o and dout must be [T, Hq, D] and lse [Hq, T]")
     for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
         if t is not None and t.shape != like.shape:
             raise ValueError("%s has another shape than its input" % name)
-    with _Launch(stream, q, k, v, o, lse, dout, cu_seqlens, dq, dk, dv, workspace) as st:
-        dq, dk, dv = (torch.empty(like.shape, dtype=torch.bfloat16, device=q.device) if t is None else t
+
+    def call(st):
+        gq, gk, gv = (torch.empty(like.shape, dtype=_BF16, device=q.device) if t is None else t
                       for t, like in ((dq, q), (dk, k), (dv, v)))
-        rows = [_token_rows(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v"), (dq, "dq"), (dk, "dk"), (dv, "dv"))]
-        ptr, strides = [r[0] for r in rows], [r[1] for r in rows]
-        ws, ws_bytes, _keep = _workspace(workspace, packed_bwd_workspace_size(T, S, Hq, D), q.device)
-        _check(lib.attn_packed_bwd(*ptr[:3], *strides[:3], _dev_tensor(o, "o", torch.bfloat16),
-                                   _dev_tensor(lse, "lse", torch.float32), _dev_tensor(dout, "dout", torch.bfloat16),
-                                   *ptr[3:], *strides[3:], _dev_tensor(cu_seqlens, "cu_seqlens", torch.int32), S, T, Hq,
-                                   Hkv, D, int(bool(causal)), int(window), float(scale), ws, ws_bytes, st))
-    return dq, dk, dv
+        (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", dev), _rows(k, "k", dev), _rows(v, "v", dev)
+        (gqp, gqs), (gkp, gks), (gvp, gvs) = _rows(gq, "dq", dev), _rows(gk, "dk", dev), _rows(gv, "dv", dev)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(lib.attn_packed_bwd_workspace_size(T, S, Hq, D), dtype=_U8, device=q.device)
+        _check(lib.attn_packed_bwd(qp, kp, vp, qs, ks, vs, _ptr(o, "o", _BF16, dev), _ptr(lse, "lse", _F32, dev),
+                                   _ptr(dout, "dout", _BF16, dev), gqp, gkp, gvp, gqs, gks, gvs,
+                                   _ptr(cu_seqlens, "cu_seqlens", _I32, dev), S, T, Hq, Hkv, D, bool(causal), window,
+                                   scale, _ptr(ws, "workspace", _U8, dev), ws.numel(), st))
+        return gq, gk, gv
+
+    return _on(dev, stream, call)
 
 
 def chunk_workspace_size(T, num_seqs, max_blocks_per_seq, page_size, Hq, Hkv, D) -> int:
@@ -437,27 +446,28 @@ def attn_chunk_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, k_n
         raise ValueError("k_new/v_new must be [T, Hkv, D]")
     if o is not None and o.shape != q.shape or lse is not None and lse.shape != (T, Hq):
         raise ValueError("o must be [T, Hq, D] and lse [T, Hq]")
-    max_blocks = block_table.shape[1]
-    with _Launch(stream, q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, k_new, v_new, o, lse, workspace) as st:
-        if o is None:
-            o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-        if lse is None and want_lse:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-        qp, qs = _token_rows(q, "q")
-        (kn, ks), (vn, vs) = ((_token_rows(k_new, "k_new"), _token_rows(v_new, "v_new")) if k_new is not None
-                              else ((None, 0), (None, 0)))
-        need = chunk_workspace_size(T, S, max_blocks, page_size, Hq, Hkv, D)
-        ws, ws_bytes, _keep = _workspace(workspace, need, q.device)
-        _check(lib.attn_chunk_paged(qp, kn, vn, qs, ks, vs, _dev_tensor(k_pages, "k_pages", torch.bfloat16),
-                                    _dev_tensor(v_pages, "v_pages", torch.bfloat16),
-                                    _dev_tensor(block_table, "block_table", torch.int32),
-                                    _dev_tensor(seq_lens, "seq_lens", torch.int32),
-                                    _dev_tensor(cu_seqlens, "cu_seqlens", torch.int32), S, T, max_blocks, num_pages,
-                                    page_size, Hq, Hkv, D, int(window), float(scale),
-                                    _dev_tensor(o, "o", torch.bfloat16),
-                                    _dev_tensor(lse, "lse", torch.float32) if lse is not None else None, ws, ws_bytes,
-                                    st))
-    return o, lse
+    max_blocks, dev = block_table.shape[1], _device_of(q)
+
+    def call(st):
+        out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device) if o is None else o
+        stats = torch.empty((T, Hq), dtype=_F32, device=q.device) if lse is None and want_lse else lse
+        qp, qs = _rows(q, "q", dev)
+        kp, ks, vp, vs = None, 0, None, 0
+        if k_new is not None:
+            (kp, ks), (vp, vs) = _rows(k_new, "k_new", dev), _rows(v_new, "v_new", dev)
+        ws = workspace
+        if ws is None:
+            need = lib.attn_chunk_workspace_size(T, S, max_blocks, page_size, Hq, Hkv, D)
+            ws = torch.empty(need, dtype=_U8, device=q.device)
+        _check(lib.attn_chunk_paged(qp, kp, vp, qs, ks, vs, _ptr(k_pages, "k_pages", _BF16, dev),
+                                    _ptr(v_pages, "v_pages", _BF16, dev), _ptr(block_table, "block_table", _I32, dev),
+                                    _ptr(seq_lens, "seq_lens", _I32, dev), _ptr(cu_seqlens, "cu_seqlens", _I32, dev), S,
+                                    T, max_blocks, num_pages, page_size, Hq, Hkv, D, window, scale,
+                                    _ptr(out, "o", _BF16, dev), None if stats is None else _ptr(stats, "lse", _F32, dev),
+                                    _ptr(ws, "workspace", _U8, dev), ws.numel(), st))
+        return out, stats
+
+    return _on(dev, stream, call)
 
 
 def attn_rope_axes(q, k, positions, sections, interleave_axes=False, per_axis_freq=False, rope_half_split=False,
@@ -469,25 +479,27 @@ def attn_rope_axes(q, k, positions, sections, interleave_axes=False, per_axis_fr
     if q.dim() != 3 or k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]):
         raise ValueError("q must be [T, Hq, D] and k [T, Hk, D]")
     T, Hq, D = q.shape
-    if positions.shape != (len(sections), T):
+    n_axes, dev = len(sections), _device_of(q)
+    if positions.shape != (n_axes, T):
         raise ValueError("positions must be [len(sections), T]")
     for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
         if t is not None and (like is None or t.shape != like.shape):
             raise ValueError("%s has another shape than its input" % name)
-    with _Launch(stream, q, k, positions, q_out, k_out) as st:
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-        if k_out is None and k is not None:
-            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
-        (qp, qs), (qo, qos) = _token_rows(q, "q"), _token_rows(q_out, "q_out")
-        (kp, ks), (ko, kos) = ((_token_rows(k, "k"), _token_rows(k_out, "k_out")) if k is not None
-                               else ((None, 0), (None, 0)))
-        sec = (ctypes.c_int * len(sections))(*(int(x) for x in sections))
-        _check(lib.attn_rope_axes(qp, qo, kp, ko, qs, qos, ks, kos, _dev_tensor(positions, "positions", torch.int32), T,
-                                  Hq, 0 if k is None else k.shape[1], D, len(sections), sec, int(bool(interleave_axes)),
-                                  int(bool(per_axis_freq)), int(bool(rope_half_split)), float(rope_base),
-                                  float(rope_pos_scale), int(bool(inverse)), st))
-    return q_out, k_out
+
+    def call(st):
+        yq = torch.empty((T, Hq, D), dtype=_BF16, device=q.device) if q_out is None else q_out
+        yk = torch.empty(k.shape, dtype=_BF16, device=q.device) if k_out is None and k is not None else k_out
+        (qp, qs), (yqp, yqs) = _rows(q, "q", dev), _rows(yq, "q_out", dev)
+        Hk, kp, ks, ykp, yks = 0, None, 0, None, 0
+        if k is not None:
+            Hk, (kp, ks), (ykp, yks) = k.shape[1], _rows(k, "k", dev), _rows(yk, "k_out", dev)
+        _check(lib.attn_rope_axes(qp, yqp, kp, ykp, qs, yqs, ks, yks, _ptr(positions, "positions", _I32, dev), T, Hq, Hk,
+                                  D, n_axes, (ctypes.c_int * n_axes)(*sections), bool(interleave_axes),
+                                  bool(per_axis_freq), bool(rope_half_split), rope_base, rope_pos_scale, bool(inverse),
+                                  st))
+        return yq, yk
+
+    return _on(dev, stream, call)
 
 
 def debug_drop_copy(enable: bool) -> None:

@@ -623,7 +623,7 @@ struct PackedCall {
 
 template <int D, bool kPaged>
 attn_status launch_packed(const PackedCall& c, cudaStream_t stream, int dev) {
-    using C = attn::FwdCfg<D>;
+    using C = attn::PackedCfg<D>;
     const int G = c.Hq / c.Hkv, TT = 128 / G;
     const long long max_keys = kPaged ? static_cast<long long>(c.max_blocks) * attn::kPageSize : c.T;
     const attn::PlanLayout L = attn::plan_layout(c.T, c.S, TT, max_keys, c.Hkv, D);
@@ -634,7 +634,7 @@ attn_status launch_packed(const PackedCall& c, cudaStream_t stream, int dev) {
     pl.header = reinterpret_cast<attn::PlanHeader*>(w + L.header);
     pl.prefix = reinterpret_cast<int*>(w + L.prefix);
     pl.items = reinterpret_cast<attn::PackedItem*>(w + L.items);
-    pl.split = reinterpret_cast<attn::SplitBlock*>(w + L.split);
+    pl.count = reinterpret_cast<int*>(w + L.count);
     pl.S = c.S;
     pl.T = c.T;
     pl.TT = TT;
@@ -668,6 +668,7 @@ attn_status launch_packed(const PackedCall& c, cudaStream_t stream, int dev) {
     p.block_table = c.block_table;
     p.o = static_cast<__nv_bfloat16*>(c.o);
     p.lse = c.lse;
+    p.count = pl.count;
     p.ws_ml = reinterpret_cast<float*>(w + L.ml);
     p.ws_o = reinterpret_cast<float*>(w + L.o);
     p.lse_t = kPaged ? c.Hq : 1;
@@ -697,13 +698,8 @@ attn_status launch_packed(const PackedCall& c, cudaStream_t stream, int dev) {
     const unsigned grid = static_cast<unsigned>(most < sms ? most : sms);
     if ((st = ensure_smem(attn::attn_packed_kernel<D, kPaged>, C::SMEM_BYTES, dev)) != ATTN_OK) return st;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t lc = dependent_launch(grid, attn::PackedCfg<D>::THREADS, C::SMEM_BYTES, stream, attr);
+    cudaLaunchConfig_t lc = dependent_launch(grid, C::THREADS, C::SMEM_BYTES, stream, attr);
     CUDA_TRY(cudaLaunchKernelEx(&lc, attn::attn_packed_kernel<D, kPaged>, tq, tk, tv, p));
-    if (L.max_slots > 0) {
-        lc = dependent_launch(static_cast<unsigned>(2 * sms), 256, 0, stream, attr);
-        CUDA_TRY(cudaLaunchKernelEx(&lc, attn::packed_merge_kernel<D>, p,
-                                    static_cast<const attn::SplitBlock*>(pl.split)));
-    }
     return ATTN_OK;
 }
 

@@ -12,8 +12,12 @@
 //     K/V tile is read once for the whole group. (G that does not divide 128 leaves 128 - G TT rows
 //     of every tile unused: 2 for G = 3, 8 for G = 5.)
 //   Items. The list of plan.cuh, walked by one persistent CTA per SM, longest items first.
-//   Parts. A block whose keys were cut into parts writes fp32 partial states that
-//     packed_merge_kernel joins in ascending order.
+//   Parts. A block whose keys were cut into parts writes fp32 partial states; of each group of 32 rows,
+//     the warp that finishes last joins them in ascending order.
+//   Sides. A block of at most TT tokens has one query tile. Both softmax warpgroups work on it, each with a
+//     copy of the queries: steps alternate between the first and the second half of the item's key tiles,
+//     and the first warpgroup joins both states out of Tensor Memory at the end. A tile of one warpgroup
+//     alone takes as long as a tile of both, so this halves the time of single tokens and short chunks.
 //   Pages. A 128-key tile of the cache is eight 16-token pages, each fetched by its own box; lane i
 //     of the producer warp looks up and issues page i.
 //   Tails. A sequence ends inside a key tile; the rows behind its end belong to another sequence or
@@ -37,12 +41,11 @@ struct PlanParams {
     PlanHeader* header;
     int* prefix;              // [S + 1] blocks (backward: tiles) of the sequences before each
     PackedItem* items;
-    SplitBlock* split;
+    int* count;               // finished parts of [slot of part 0][K/V head][softmax warp]
     PackedTile* tiles;        // backward: natural order
     int* order;               // backward: tile numbers, most query tiles first
     int S, T, TT, Hkv, causal, window;
     int max_len;              // paged: tokens a block-table row can hold
-    int max_slots;
 };
 
 constexpr int kPlanThreads = 1024;
@@ -77,25 +80,30 @@ __device__ __forceinline__ int plan_scan(int x, int* warp_sums, int& total) {
     return out;
 }
 
-// Builds the item list (one CTA). kBwd: the backward's tiles. Three walks over the blocks: the sum
-// and the largest of their key tiles (the split rule), the histogram, the list. Runs in a few
-// microseconds; what it costs is the latency of its steps, not the number of blocks.
+// Builds the item list (one CTA). kBwd: the backward's tiles. Three or four walks over the blocks: the
+// sum and the largest of their key tiles, the histogram (with and without cutting, where some block is
+// long enough for it), the list. Runs in a few microseconds; what it costs is the latency of its steps,
+// not the number of blocks.
+//
+// Whether to cut: CTA c takes items c, 2 G - 1 - c, ... of the descending list, so no CTA gets more key
+// tiles than the sum of every G-th item. Blocks are cut when that sum with all parts within the limit,
+// plus the cost of joining, is below the sum without.
 template <bool kBwd>
 __device__ void build_plan(const PlanParams& p) {
     __shared__ int s_hist[kPlanBuckets];
     __shared__ int s_prefix[kPlanSmemSeqs + 1];
     __shared__ int s_warp[33];
     __shared__ unsigned long long s_sum;
-    __shared__ int s_max, s_slots, s_split;
+    __shared__ int s_max, s_slots, s_load[2];
     const int tid = threadIdx.x;
     const int tok = kBwd ? 128 : 2 * p.TT;  // tokens per block
     int* pre = p.S <= kPlanSmemSeqs ? s_prefix : p.prefix;
     if (tid == 0) {
         s_sum = 0;
         s_max = 1;
-        s_slots = s_split = 0;
+        s_slots = 0;
+        s_load[0] = s_load[1] = 0;
     }
-    s_hist[tid] = 0;
     int carry = 0, bad = 0;
     for (int base = 0; base < p.S; base += kPlanThreads) {
         const int s = base + tid;
@@ -184,19 +192,47 @@ __device__ void build_plan(const PlanParams& p) {
     auto bucket = [&](int tiles) {
         return kPlanBuckets - 1 - static_cast<int>(static_cast<long long>(tiles) * (kPlanBuckets - 1) / longest);
     };
-    auto parts_of = [&](const Block& x) { return kBwd ? 1 : plan_parts(x.tiles, limit); };
-
-    for (int b = tid; b < n_blocks; b += kPlanThreads) {
-        const Block x = get(b);
-        const int parts = parts_of(x), q = x.tiles / parts, r = x.tiles % parts;
-        if (r > 0) atomicAdd(&s_hist[bucket(q + 1)], r);
-        atomicAdd(&s_hist[bucket(q)], parts - r);
+    int n_items = 0;
+    bool cut = false;
+    // counts the items of each length into s_hist and turns that into the first position of each length
+    auto sort_items = [&](bool with_parts) {
+        s_hist[tid] = 0;
+        __syncthreads();
+        for (int b = tid; b < n_blocks; b += kPlanThreads) {
+            const Block x = get(b);
+            const int parts = with_parts ? plan_parts(x.tiles, limit) : 1, q = x.tiles / parts, r = x.tiles % parts;
+            if (r > 0) atomicAdd(&s_hist[bucket(q + 1)], r);
+            atomicAdd(&s_hist[bucket(q)], parts - r);
+        }
+        __syncthreads();
+        const int mine_n = s_hist[tid];
+        const int start = plan_scan(mine_n, s_warp, n_items);
+        s_hist[tid] = start;
+        if (!kBwd && longest > limit && mine_n > 0) {
+            // G-th items of this length
+            const int first = plan_ceil_div(static_cast<long long>(start) * p.Hkv, kPlanSms);
+            const int last = plan_ceil_div(static_cast<long long>(start + mine_n) * p.Hkv, kPlanSms);
+            const int len = static_cast<int>(plan_ceil_div(static_cast<long long>(kPlanBuckets - 1 - tid) * longest, kPlanBuckets - 1));
+            if (last > first) atomicAdd(&s_load[with_parts], (last - first) * len);
+        }
+        __syncthreads();
+    };
+    if (!kBwd && longest > limit) {
+        sort_items(true);
+        cut = true;
+        const int with = s_load[1] + kPlanJoinTiles;
+        const int start = s_hist[tid], items_cut = n_items;
+        sort_items(false);
+        if (with < s_load[0]) {
+            s_hist[tid] = start;
+            n_items = items_cut;
+        } else {
+            cut = false;
+        }
+        __syncthreads();
+    } else {
+        sort_items(false);
     }
-    __syncthreads();
-    int n_items;
-    const int start = plan_scan(s_hist[tid], s_warp, n_items);
-    s_hist[tid] = start;
-    __syncthreads();
 
     for (int b = tid; b < n_blocks; b += kPlanThreads) {
         const Block x = get(b);
@@ -209,7 +245,7 @@ __device__ void build_plan(const PlanParams& p) {
             p.tiles[b] = t;
             p.order[atomicAdd(&s_hist[bucket(x.tiles)], 1)] = b;
         } else {
-            const int parts = parts_of(x);
+            const int parts = cut ? plan_parts(x.tiles, limit) : 1;
             const int row0 = p.cu[x.s];
             const int n = p.cu[x.s + 1] - row0;
             PackedItem it;
@@ -220,7 +256,7 @@ __device__ void build_plan(const PlanParams& p) {
             it.slot = 0;
             if (parts > 1) {
                 it.slot = atomicAdd(&s_slots, parts);
-                p.split[atomicAdd(&s_split, 1)] = SplitBlock{it.q_row, x.n, it.slot, parts};
+                for (int i = 0; i < p.Hkv * kPlanWarps; ++i) p.count[static_cast<size_t>(it.slot) * p.Hkv * kPlanWarps + i] = 0;
             }
             const int jb =
                 x.kv_len < 0 ? 0 : key_tiles(it.pos0, it.pos0 + x.n - 1, x.kv_len, p.causal, p.window).jb;
@@ -236,7 +272,7 @@ __device__ void build_plan(const PlanParams& p) {
     }
     __syncthreads();
     if (tid == 0) {
-        PlanHeader h{n_items, s_split, 0, 0};
+        PlanHeader h{n_items, s_slots, 0, 0};
         *p.header = h;
     }
 }
@@ -306,6 +342,7 @@ struct PackedParams {
     const int32_t* block_table;  // paged
     __nv_bfloat16* o;            // [T, Hq, D]
     float* lse;                  // element (token t, head h) at t * lse_t + h * lse_h, or nullptr
+    int* count;                  // finished parts of [slot of part 0][Hkv][softmax warp]
     float* ws_ml;                // partial states: [slot][Hkv][256 rows][2] (max in log2 units, sum)
     float* ws_o;                 // [slot][Hkv][256 rows][D] unnormalised
     long long lse_t, lse_h;
@@ -324,9 +361,12 @@ struct alignas(16) PackedWork {
     int J0, T;          // key tiles of the item
     int g, parts;       // K/V head; parts of the block
     int tok[2];         // tokens of query tile i (0: absent)
-    int state;          // partial-state slot (blocks of more than one part)
-    int pad;
-    int a[2], e[2];     // visible key tiles of query tile i: [J0 + a, J0 + e)
+    int slot, part;     // partial-state slot of part 0 (blocks of more than one part), and this part
+    int a[2], e[2];     // steps of query tile i: [a, e), of a two-sided item every second of them
+    int half;           // two-sided: key tiles of the first side; else 0
+    int pad[3];
+    // The key tile of step u, counted from J0.
+    __device__ __forceinline__ int tile(int u) const { return half > 0 ? (u & 1) * half + (u >> 1) : u; }
 };
 
 __device__ __forceinline__ PackedWork decode_item(const PackedParams& p, const int4& lo, const int4& hi, int g) {
@@ -340,8 +380,8 @@ __device__ __forceinline__ PackedWork decode_item(const PackedParams& p, const i
     w.T = hi.y;
     const int n_tok = hi.z & 1023;
     w.parts = ((hi.z >> 20) & 1023) + 1;
-    w.state = hi.w + ((hi.z >> 10) & 1023);
-    w.pad = 0;
+    w.slot = hi.w;
+    w.part = (hi.z >> 10) & 1023;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int n = min(p.TT, n_tok - i * p.TT);
@@ -357,6 +397,13 @@ __device__ __forceinline__ PackedWork decode_item(const PackedParams& p, const i
             }
         }
     }
+    w.half = 0;
+    if (w.tok[1] == 0 && w.T > 1) {
+        w.half = (w.T + 1) / 2;
+        w.a[1] = 1;
+        w.e[0] = ((w.T - 1) & ~1) + 1;
+        w.e[1] = w.T - (w.T & 1);
+    }
     return w;
 }
 
@@ -366,7 +413,9 @@ template <int NK, int NV>
 struct PackedBarriers : FwdBarriers<NK, NV> {
     uint64_t work_full[kWorkRing], work_empty[kWorkRing];
     uint64_t s_free[2], pv_done[2], drain_outputs;  // kSplitP
+    uint64_t side_full, side_empty;  // the second side's statistics
     PackedWork work[kWorkRing];
+    float2 side_ml[128];
 };
 
 // Sets the columns of s outside [lo, hi] to -inf: a bit per column, 32 columns at a time (two
@@ -383,16 +432,100 @@ __device__ __forceinline__ void mask_columns(float (&s)[N], int lo, int hi) {
     }
 }
 
+// Called by a softmax warp that has stored its 32 rows' partial states of one part (rows of query tile
+// wg from 32 quad on; q_row: the tile's first token): when it is the last of the block's parts, it joins them, M = max m_i,
+// L = sum 2^(m_i - M) l_i, O = sum 2^(m_i - M) o_i / L, LSE = (M + log2 L) ln 2, in ascending order of i.
+// The statistics go a row to a lane, the outputs a row to the warp, four rows and parts at a time: what
+// counts is how many loads are in flight.
+template <int D>
+__device__ __noinline__ void join_parts(const PackedParams& p, int g, int q_row, int tok, int slot, int parts, int wg, int quad) {
+    constexpr int PER = D / 32;  // columns of a lane
+    const int lane = threadIdx.x & 31;
+    if (tok * p.G <= quad * 32) return;  // none of its rows is live
+    __threadfence();  // this lane's states before the count
+    __syncwarp();
+    int last = 0;
+    if (lane == 0)
+        last = atomicAdd(p.count + (static_cast<size_t>(slot) * p.Hkv + g) * kPlanWarps + wg * 4 + quad, 1) == parts - 1;
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    __threadfence();  // the count before the other parts' states
+    const size_t step = static_cast<size_t>(p.Hkv) * 256;  // rows from one part's state to the next
+    const int rows = min(32, tok * p.G - quad * 32);  // live rows of this warp
+    const size_t row0 = (static_cast<size_t>(slot) * p.Hkv + g) * 256 + wg * 128 + quad * 32;
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + row0;
+    float M = -INFINITY, inv = 0.f;  // of row `lane`
+    if (lane < rows) {
+        float L = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(ml + lane + i * step).x);
+#pragma unroll 8
+        for (int i = 0; i < parts; ++i) {
+            const float2 s = __ldcg(ml + lane + i * step);
+            L = fmaf(s.x == -INFINITY ? 0.f : ptx::ex2(s.x - M), s.y, L);  // -inf: none of the row's keys, and no output
+        }
+        inv = L > 0.f ? 1.f / L : 0.f;
+        const int r = quad * 32 + lane, t = r / p.G, h = g * p.G + r - t * p.G;
+        const size_t row = static_cast<size_t>(q_row) + t;
+        if (p.lse != nullptr) p.lse[row * p.lse_t + h * p.lse_h] = L > 0.f ? (M + ptx::lg2(L)) * kLn2 : -INFINITY;
+    }
+    constexpr int R = 4;         // rows at a time
+    for (int r0 = 0; r0 < rows; r0 += R) {
+        float acc[R][PER], Mr[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            Mr[j] = __shfl_sync(0xffffffffu, M, min(r0 + j, rows - 1));
+#pragma unroll
+            for (int c = 0; c < PER; ++c) acc[j][c] = 0.f;
+        }
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) {
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                const size_t at = min(r0 + j, rows - 1) + i * step;
+                const float m = __ldcg(ml + at).x;
+                const float* o = p.ws_o + (row0 + at) * D + lane * PER;
+                float v[PER];
+                if constexpr (PER == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(o));
+                    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2*>(o));
+                    v[0] = x.x; v[1] = x.y;
+                }
+                const float w = ptx::ex2(m - Mr[j]);
+#pragma unroll
+                for (int c = 0; c < PER; ++c) acc[j][c] = m == -INFINITY ? acc[j][c] : fmaf(w, v[c], acc[j][c]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const float iv = __shfl_sync(0xffffffffu, inv, min(r0 + j, rows - 1));
+            if (r0 + j >= rows) continue;
+            const int r = quad * 32 + r0 + j, t = r / p.G, h = g * p.G + r - t * p.G;
+            uint32_t* out = reinterpret_cast<uint32_t*>(p.o + ((static_cast<size_t>(q_row) + t) * p.Hq + h) * D + lane * PER);
+            if constexpr (PER == 4)
+                *reinterpret_cast<uint2*>(out) = make_uint2(ptx::pack_bf16x2(acc[j][0] * iv, acc[j][1] * iv),
+                                                            ptx::pack_bf16x2(acc[j][2] * iv, acc[j][3] * iv));
+            else
+                *out = ptx::pack_bf16x2(acc[j][0] * iv, acc[j][1] * iv);
+        }
+    }
+}
+
 template <int D>
 struct PackedCfg {
     static constexpr bool kSplitP = D == 64;
     static constexpr int THREADS = FwdCfg<D>::THREADS + (kSplitP ? 32 : 0);  // a second MMA issuer
+    static constexpr int BAR_BYTES = 2048;
+    // tiles, barriers, and the gap in front of the tiles' 1024-byte boundary
+    static constexpr int SMEM_BYTES = FwdCfg<D>::SMEM_TILES * FwdCfg<D>::TILE_BYTES + BAR_BYTES + 1024;
+    static_assert(SMEM_BYTES <= 232448, "shared memory above 227 KiB per CTA");
 };
 
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
     attn_packed_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const PackedParams p) {
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PackedParams p) {
     using C = FwdCfg<D>;
     constexpr int NK = C::NK, NV = C::NV;
     constexpr int kPages = C::BN / kPageSize;  // pages of a key tile
@@ -405,7 +538,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
     uint8_t* sK = sQ + C::QT * C::TILE_BYTES;
     uint8_t* sV = sK + NK * C::TILE_BYTES;
     auto* bar = reinterpret_cast<PackedBarriers<NK, NV>*>(sV + NV * C::TILE_BYTES);
-    static_assert(sizeof(PackedBarriers<NK, NV>) <= 1024, "barrier block larger than its reserved bytes");
+    static_assert(sizeof(PackedBarriers<NK, NV>) <= PackedCfg<D>::BAR_BYTES, "barrier block larger than its reserved bytes");
     volatile int* abort_flag = &bar->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -434,6 +567,8 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
         }
         ptx::mbar_init(&bar->drain, 1);
         ptx::mbar_init(&bar->drain_outputs, 1);
+        ptx::mbar_init(&bar->side_full, 128);
+        ptx::mbar_init(&bar->side_empty, 128);
         bar->abort = 0;
         ptx::fence_mbar_init();
     }
@@ -489,7 +624,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
 #pragma unroll
                     for (int r = 0; r < C::NREG; ++r)
                         ptx::tma_load_3d(sQ + i * C::TILE_BYTES + r * C::REGION_BYTES, &tm_q, &bar->q_loaded[i], r * 64,
-                                         x.g * p.G, x.q_row + i * p.TT);
+                                         x.g * p.G, x.q_row + (x.half > 0 ? 0 : i * p.TT));
                 }
                 ++kq[i];
             }
@@ -500,22 +635,22 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
             // lane i of a paged tile: page i of the next tile, looked up one tile ahead
             int page = 0;
             auto look_up = [&](int u) {
-                const int pg = (x.J0 + u) * kPages + lane;
+                const int pg = (x.J0 + x.tile(u)) * kPages + lane;
                 return (lane < kPages && u < x.T && pg < seq_pages && pg >= first_page) ? bt[pg] : -1;
             };
             if constexpr (kPaged) page = look_up(0);
             for (int u = 0; u < x.T && ok; ++u, ++g) {
-                const int k0 = (x.J0 + u) * C::BN;
+                const int jt = x.J0 + x.tile(u), k0 = jt * C::BN;
                 const int sk = g % NK, sv = g % NV;
                 if (g >= NK && !ptx::mbar_wait_warp(&bar->k_empty[sk], ((g / NK) - 1) & 1, abort_flag)) { ok = false; break; }
                 const bool drop = p.debug_drop_copy && g == 0 && blockIdx.x == 0;
                 int z = 0, pages = 0;
                 if constexpr (kPaged) {
-                    pages = min(kPages, seq_pages - (x.J0 + u) * kPages);
+                    pages = min(kPages, seq_pages - jt * kPages);
                     // a page that is invalid (flagged) or before the window is read as zeros, by a box
                     // outside the tensor: what its memory holds cannot reach a product
                     const bool valid = page >= 0 && page < p.num_pages;
-                    if (lane < pages && !valid && (x.J0 + u) * kPages + lane >= first_page) raise_status(kStatusBadPage);
+                    if (lane < pages && !valid && jt * kPages + lane >= first_page) raise_status(kStatusBadPage);
                     z = valid ? page * p.Hkv + x.g : -1;
                     page = look_up(u + 1);
                     if (lane == 0) ptx::mbar_arrive_expect_tx(&bar->k_full[sk], pages * kPageSize * C::ROW_BYTES);
@@ -644,12 +779,14 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
             const int ws = rnd % kWorkRing;
             if (!ptx::mbar_wait_warp(&bar->work_full[ws], (rnd / kWorkRing) & 1, abort_flag)) { ok = false; break; }
             const PackedWork& x = bar->work[ws];
-            const int T = x.T, key0 = x.J0 * C::BN;
+            const int T = x.T, key0 = x.J0 * C::BN, half = x.half;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 a[i] = x.a[i];
                 e[i] = x.e[i];
-                seen[i] = (p.causal ? min(x.kv_len, x.pos0 + i * p.TT + x.tok[i]) : x.kv_len) - key0;
+                const int q_tile = half > 0 ? 0 : i;
+                seen[i] = (p.causal ? min(x.kv_len, x.pos0 + q_tile * p.TT + x.tok[q_tile]) : x.kv_len) - key0 -
+                          (half > 0 && i == 1 ? half * C::BN : 0);
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bar->work_empty[ws]);
@@ -663,9 +800,10 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (outputs && ok && u >= a[i] && u < e[i])
-                        ok = output_tile(i, u == a[i], u == e[i] - 1, seen[i] - u * C::BN);
-                    if (scores && ok && us >= a[i] && us < e[i]) ok = score_tile(i, us == a[i], us == e[i] - 1);
+                    if (outputs && ok && u >= a[i] && u < e[i] && (half == 0 || (u & 1) == i))
+                        ok = output_tile(i, u == a[i], u == e[i] - 1, seen[i] - (half > 0 ? u >> 1 : u) * C::BN);
+                    if (scores && ok && us >= a[i] && us < e[i] && (half == 0 || (us & 1) == i))
+                        ok = score_tile(i, us == a[i], us == e[i] - 1);
                 }
                 if (!ok) break;
                 if (outputs && u >= 0) {
@@ -707,7 +845,12 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
         const float sl = p.scale_log2;
         const int my_tok = r / p.G, my_head = r - my_tok * p.G;  // this row's token in the tile and head in the group
         bool ok = true;
-        int kq = 0, cw = 0;
+        // Barrier parities, a bit each (a wait for the phase before is one for the other parity, which a
+        // fresh barrier passes): this warpgroup's next key tile, its items; the second warpgroup's key
+        // tiles and items; two-sided items.
+        constexpr uint32_t kTiles = 1, kItems = 2, kTiles1 = 4, kItems1 = 8, kSides = 16;
+        uint32_t par = 0;
+        auto parity = [&](uint32_t bit) { return (par & bit) ? 1u : 0u; };
         int g = 0;  // key tiles of the items before
         for (int rnd = 0, it = blockIdx.x; ok && it < n_items; it = item_of_round(++rnd, blockIdx.x, gridDim.x)) {
             const int ws = rnd % kWorkRing;
@@ -717,16 +860,19 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&bar->work_empty[ws]);
             };
-            const int n = wg ? x.e[1] - x.a[1] : x.e[0] - x.a[0];  // key tiles of this query tile
-            const int jb = x.J0 + (wg ? x.a[1] : x.a[0]);
-            const int tok = wg ? x.tok[1] : x.tok[0];
+            const bool two_sided = x.half > 0;
+            const int q_tile = two_sided ? 0 : wg;
+            const int a = x.a[wg], first = two_sided ? wg * x.half : a;  // first step and first key tile
+            const int n1 = two_sided ? x.T - x.half : x.e[1] - x.a[1];
+            const int n = wg ? n1 : two_sided ? x.half : x.e[0] - x.a[0];  // key tiles of this warpgroup
+            const int jb = x.J0 + first, stride = two_sided ? 2 : 1;
+            const int tok = x.tok[q_tile];
             const bool live = my_tok < tok;  // tok <= TT: rows past G * TT never are
-            const int i_pos = x.pos0 + wg * p.TT + my_tok;
-            const int pos_first = x.pos0 + wg * p.TT;
+            const int pos_first = x.pos0 + q_tile * p.TT, i_pos = pos_first + my_tok;
             float m_used = -INFINITY, l = 0.f;
             for (int c = 0; ok && c < n; ++c) {
                 const int j0 = (jb + c) * C::BN;
-                if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->s_full[wg], (cw + c) & 1, abort_flag))) { ok = false; break; }
+                if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->s_full[wg], parity(kTiles), abort_flag))) { ok = false; break; }
                 ptx::tc_fence_after();
                 uint32_t sv[C::BN];
                 ptx::tmem_ld128(t_s, sv);
@@ -793,7 +939,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 l = l * alpha + (sum.x + sum.y);
                 if constexpr (kSplitP) {
                     // P and O are free once the product before has completed
-                    if (cw + c > 0 && !__all_sync(0xffffffffu, ptx::mbar_wait(&bar->pv_done[wg], (cw + c - 1) & 1, abort_flag))) { ok = false; break; }
+                    if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->pv_done[wg], parity(kTiles) ^ 1, abort_flag))) { ok = false; break; }
                     ptx::tc_fence_after();
                 }
                 ptx::tmem_st64(t_p, pk);
@@ -801,8 +947,8 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 // query tiles may do it: the same zeros, before either P is handed over)
                 const int tail = x.kv_len - j0;
                 if (tail < C::BN && (tail & 15)) {
-                    const int sv_st = (g + jb - x.J0 + c) % NV;
-                    if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->v_full[sv_st], ((g + jb - x.J0 + c) / NV) & 1, abort_flag))) { ok = false; break; }
+                    const int gs = g + a + c * stride, sv_st = gs % NV;
+                    if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->v_full[sv_st], (gs / NV) & 1, abort_flag))) { ok = false; break; }
                     const uint32_t base = ptx::smem_u32(sV + sv_st * C::TILE_BYTES) + tail * 128;
                     const int chunks = (16 - (tail & 15)) * 8;  // 16-byte pieces per region
                     for (int t = r; t < chunks * C::NREG; t += 128)
@@ -827,21 +973,24 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 }
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(&bar->p_full[wg]);
+                par ^= kTiles;
             }
             if (!ok) break;
             g += x.T;
+            if (n1 > 0) par ^= kItems1;
+            if (n1 & 1) par ^= kTiles1;
             if (tok == 0) {
                 release_work();
                 continue;
             }
             const size_t prow =
-                ((static_cast<size_t>(x.state) * p.Hkv + x.g) * 256 + wg * 128 + r);  // partial-state row
+                ((static_cast<size_t>(x.slot + x.part) * p.Hkv + x.g) * 256 + wg * 128 + r);  // partial-state row
             if (n == 0) {
                 // an invalid length, or a part none of whose keys this query tile sees
                 if (x.kv_len < 0) {
                     if (r == 0 && wg == 0 && x.g == 0) raise_status(kStatusBadSeqLen);
                     if (live) {
-                        const size_t row = static_cast<size_t>(x.q_row + wg * p.TT + my_tok);
+                        const size_t row = static_cast<size_t>(x.q_row + q_tile * p.TT + my_tok);
                         const int h = x.g * p.G + my_head;
                         uint4* dst = reinterpret_cast<uint4*>(p.o + (row * p.Hq + h) * D);
                         for (int k = 0; k < D / 8; ++k)
@@ -852,63 +1001,99 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                     p.ws_ml[prow * 2] = -INFINITY;
                     p.ws_ml[prow * 2 + 1] = 0.f;
                 }
+                if (x.kv_len >= 0) join_parts<D>(p, x.g, x.q_row + wg * p.TT, tok, x.slot, x.parts, wg, warp & 3);
                 release_work();
                 continue;
             }
-            cw += n;
+            if (two_sided && wg == 1) {
+                // hand the statistics to the first warpgroup, which reads both accumulators
+                if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->side_empty, parity(kSides) ^ 1, abort_flag))) { ok = false; break; }
+                bar->side_ml[r] = make_float2(m_used, l);
+                ptx::mbar_arrive(&bar->side_full);
+                par ^= kSides | kItems;
+                release_work();
+                continue;
+            }
             // ---- epilogue: O out of TMEM; normalised to the output, or as a partial state
-            if (!__all_sync(0xffffffffu, kSplitP ? ptx::mbar_wait(&bar->pv_done[wg], (cw - 1) & 1, abort_flag)
-                                                 : ptx::mbar_wait(&bar->o_final[wg], kq & 1, abort_flag))) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, kSplitP ? ptx::mbar_wait(&bar->pv_done[wg], parity(kTiles) ^ 1, abort_flag)
+                                                 : ptx::mbar_wait(&bar->o_final[wg], parity(kItems), abort_flag))) { ok = false; break; }
             ptx::tc_fence_after();
+            float w0 = 1.f, w1 = 0.f;  // weights of the sides' accumulators
+            if (two_sided) {
+                if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->side_full, parity(kSides), abort_flag))) { ok = false; break; }
+                par ^= kSides;
+                const float2 other = bar->side_ml[r];
+                ptx::mbar_arrive(&bar->side_empty);
+                if (!__all_sync(0xffffffffu, kSplitP ? ptx::mbar_wait(&bar->pv_done[1], parity(kTiles1) ^ 1, abort_flag)
+                                                     : ptx::mbar_wait(&bar->o_final[1], parity(kItems1) ^ 1, abort_flag))) { ok = false; break; }
+                ptx::tc_fence_after();
+                const float m = fmaxf(m_used, other.x);
+                w0 = m_used == -INFINITY ? 0.f : ptx::ex2(m_used - m);
+                w1 = other.x == -INFINITY ? 0.f : ptx::ex2(other.x - m);
+                l = l * w0 + other.y * w1;
+                m_used = m;
+            }
+            // 32 columns of O, of a two-sided item both sides weighted
+            auto load_output = [&](int c0, uint32_t (&v)[32]) {
+                ptx::tmem_ld32(t_o + c0, v);
+                if (two_sided) {
+                    uint32_t v1[32];
+                    ptx::tmem_ld32(tmem + lane_base + C::tmem_o(1) + c0, v1);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        v[k] = __float_as_uint(__uint_as_float(v[k]) * w0 + __uint_as_float(v1[k]) * w1);
+                }
+            };
+            auto output_read = [&]() {
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bar->o_empty[wg]);
+                if (two_sided) ptx::mbar_arrive(&bar->o_empty[1]);
+            };
             if (x.parts > 1) {
 #pragma unroll
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t v[32];
-                    ptx::tmem_ld32(t_o + cc * 32, v);
+                    load_output(cc * 32, v);
                     if (live) {
                         uint32_t* dst = reinterpret_cast<uint32_t*>(p.ws_o + prow * D + cc * 32);  // 256-byte aligned rows
 #pragma unroll
                         for (int k = 0; k < 32; k += 8) ptx::st_global_v8(dst + k, v + k);
                     }
                 }
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(&bar->o_empty[wg]);
+                output_read();
                 if (live) {
                     p.ws_ml[prow * 2] = m_used;
                     p.ws_ml[prow * 2 + 1] = l;
                 }
+                join_parts<D>(p, x.g, x.q_row + q_tile * p.TT, tok, x.slot, x.parts, wg, warp & 3);
             } else {
-                uint32_t w[D / 2];
                 const float inv_l = l > 0.f ? 1.f / l : 0.f;
+                const size_t row = static_cast<size_t>(x.q_row + q_tile * p.TT + my_tok);
+                const int h = x.g * p.G + my_head;
+                uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row * p.Hq + h) * D);
+                const bool sectors = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;  // whole 32-byte sectors
 #pragma unroll
                 for (int cc = 0; cc < D / 32; ++cc) {
-                    uint32_t v[32];
-                    ptx::tmem_ld32(t_o + cc * 32, v);
+                    uint32_t v[32], w[16];
+                    load_output(cc * 32, v);
+                    if (cc == D / 32 - 1) output_read();
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        w[cc * 16 + k] =
-                            ptx::pack_bf16x2(__uint_as_float(v[2 * k]) * inv_l, __uint_as_float(v[2 * k + 1]) * inv_l);
-                }
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(&bar->o_empty[wg]);
-                if (live) {
-                    const size_t row = static_cast<size_t>(x.q_row + wg * p.TT + my_tok);
-                    const int h = x.g * p.G + my_head;
-                    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row * p.Hq + h) * D);
-                    // whole 32-byte sectors where the tensor's alignment allows it
-                    if ((reinterpret_cast<uintptr_t>(p.o) & 31) == 0) {
+                        w[k] = ptx::pack_bf16x2(__uint_as_float(v[2 * k]) * inv_l, __uint_as_float(v[2 * k + 1]) * inv_l);
+                    if (!live) continue;
+                    if (sectors) {
 #pragma unroll
-                        for (int k = 0; k < D / 2; k += 8) ptx::st_global_v8(dst + k, w + k);
+                        for (int k = 0; k < 16; k += 8) ptx::st_global_v8(dst + cc * 16 + k, w + k);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < D / 2; k += 4)
-                            *reinterpret_cast<uint4*>(dst + k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+                        for (int k = 0; k < 16; k += 4)
+                            *reinterpret_cast<uint4*>(dst + cc * 16 + k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
                     }
-                    if (p.lse != nullptr)
-                        p.lse[row * p.lse_t + h * p.lse_h] = l > 0.f ? (m_used + ptx::lg2(l)) * kLn2 : -INFINITY;
                 }
+                if (live && p.lse != nullptr)
+                    p.lse[row * p.lse_t + h * p.lse_h] = l > 0.f ? (m_used + ptx::lg2(l)) * kLn2 : -INFINITY;
             }
-            ++kq;
+            par ^= kItems;
             release_work();
         }
         if (!ok) {
@@ -922,54 +1107,6 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
     if (warp == C::MMA_WARP) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, C::TMEM_COLS);
-    }
-}
-
-// Joins the partial states of every block that was cut into parts, in ascending order: M = max m_i,
-// L = sum 2^(m_i - M) l_i, O = sum 2^(m_i - M) o_i / L, LSE = (M + log2 L) ln 2. One warp per row,
-// over all rows of all such blocks (none for most calls).
-template <int D>
-__global__ void __launch_bounds__(256) packed_merge_kernel(const PackedParams p, const SplitBlock* split) {
-    ptx::grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    constexpr int PER = D / 32;
-    const long long rows = static_cast<long long>(p.header->n_split) * p.Hkv * 256;
-    const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
-    for (long long w = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); w < rows; w += warps) {
-        const int r = static_cast<int>(w & 255);
-        const long long bg = w >> 8;
-        const int g = static_cast<int>(bg % p.Hkv);
-        const SplitBlock b = split[bg / p.Hkv];
-        const int in_tile = (r & 127) / p.G;
-        const int tok = (r >> 7) * p.TT + in_tile;
-        if (in_tile >= p.TT || tok >= b.n_tok) continue;
-        const size_t step = static_cast<size_t>(p.Hkv) * 256;  // rows from one part's state to the next
-        const size_t row0 = (static_cast<size_t>(b.slot) * p.Hkv + g) * 256 + r;
-        float M = -INFINITY;
-        for (int i = lane; i < b.parts; i += 32) M = fmaxf(M, p.ws_ml[(row0 + i * step) * 2]);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        float acc[PER], L = 0.f;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-        for (int i = 0; i < b.parts; ++i) {
-            const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + (row0 + i * step) * 2);
-            if (ml.x == -INFINITY) continue;  // the part holds none of the row's keys (and no output)
-            const float wt = ptx::ex2(ml.x - M);
-            L += wt * ml.y;
-            const float* oc = p.ws_o + (row0 + i * step) * D + lane * PER;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] += wt * oc[e];
-        }
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        const int h = g * p.G + (r & 127) - in_tile * p.G;
-        const size_t row = static_cast<size_t>(b.q_row) + tok;
-        __nv_bfloat16* orow = p.o + (row * p.Hq + h) * D + lane * PER;
-#pragma unroll
-        for (int e = 0; e < PER; e += 2)
-            *reinterpret_cast<uint32_t*>(orow + e) = ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-        if (p.lse != nullptr && lane == 0)
-            p.lse[row * p.lse_t + h * p.lse_h] = L > 0.f ? (M + ptx::lg2(L)) * kLn2 : -INFINITY;
     }
 }
 

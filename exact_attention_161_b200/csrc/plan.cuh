@@ -8,9 +8,10 @@
 //             range of 128-key tiles. Each item stands for every K/V head.
 //   backward  an item is one 128-key tile of one sequence.
 // Items are listed longest first (a counting sort by their key or query tiles), so that CTAs that
-// take them in rounds finish together. A forward block whose keys are more than a CTA's fair share
-// of the whole call is cut into parts along the keys; the parts' softmax states are merged
-// afterwards in ascending order, so the result depends on the lengths alone, not on timing.
+// take them in rounds finish together. Where the longest blocks would leave most CTAs idle at the end,
+// long forward blocks are cut into parts along the keys; the warp that finishes a block's last part
+// joins the parts' softmax states in ascending order, so the result depends on the lengths alone, not
+// on timing.
 //
 // The index arithmetic is host code too, so that it can be checked without a GPU.
 #pragma once
@@ -30,10 +31,12 @@ constexpr int kPlanWaves = 2;        // parts per CTA the split rule aims at
 constexpr int kPlanMinTiles = 4;     // no part is planned shorter than this many key tiles
 constexpr int kPlanMaxParts = 1023;  // of one block (the record's part fields are 10 bits wide)
 constexpr int kPlanBuckets = 1024;   // of the counting sort
+constexpr int kPlanJoinTiles = 6;    // what cutting costs a call (partial states, joining them), in key tiles
 
 ATTN_HD int plan_min(int a, int b) { return a < b ? a : b; }
 ATTN_HD int plan_max(int a, int b) { return a > b ? a : b; }
 ATTN_HD int plan_ceil(int a, int b) { return (a + b - 1) / b; }
+ATTN_HD int plan_ceil_div(long long a, int b) { return static_cast<int>((a + b - 1) / b); }
 
 // One forward item: tokens [q_row, q_row + n_tok) of the packed queries, the first of them at
 // position pos0 of its sequence, against key tiles [jb, jb + n_tiles) of the sequence.
@@ -51,11 +54,6 @@ ATTN_HD int item_part(const PackedItem& x) { return (x.meta >> 10) & 1023; }
 ATTN_HD int item_parts(const PackedItem& x) { return ((x.meta >> 20) & 1023) + 1; }
 ATTN_HD int make_meta(int n_tok, int part, int parts) { return n_tok | (part << 10) | ((parts - 1) << 20); }
 
-// A block that was cut into parts, for the merge.
-struct SplitBlock {
-    int q_row, n_tok, slot, parts;
-};
-
 // One 128-row tile of a packed sequence, for the backward: rows [row0 + 128 t, ...) of a sequence
 // of n rows that starts at row0; base is the number of the sequence's first tile.
 struct PackedTile {
@@ -65,7 +63,7 @@ struct PackedTile {
 // Head of a plan in the workspace.
 struct PlanHeader {
     int n_items;   // forward items (each for every K/V head); backward tiles
-    int n_split;   // blocks cut into parts
+    int n_slots;   // partial-state slots in use
     int bad;       // the offsets are invalid: there are no items
     int pad;
 };
@@ -119,11 +117,12 @@ ATTN_HD long long plan_slots(long long blocks, long long max_tiles, int Hkv) {
     return a < b ? a : b;
 }
 
+constexpr int kPlanWarps = 8;  // softmax warps, each with a counter of the parts it has finished
 ATTN_HD size_t plan_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Byte offsets of a forward plan in the workspace.
 struct PlanLayout {
-    size_t header, prefix, items, split, ml, o, total;
+    size_t header, prefix, items, count, ml, o, total;
     long long max_items, max_slots;
 };
 // T packed query tokens in S sequences, TT tokens to a query tile, at most max_keys keys to a sequence.
@@ -135,8 +134,8 @@ ATTN_HD PlanLayout plan_layout(long long T, long long S, int TT, long long max_k
     L.header = 0;
     L.prefix = 256;
     L.items = L.prefix + plan_up(static_cast<size_t>(S + 1) * sizeof(int));
-    L.split = L.items + plan_up(static_cast<size_t>(L.max_items) * sizeof(PackedItem));
-    L.ml = L.split + plan_up(static_cast<size_t>(L.max_slots) * sizeof(SplitBlock));
+    L.count = L.items + plan_up(static_cast<size_t>(L.max_items) * sizeof(PackedItem));
+    L.ml = L.count + plan_up(static_cast<size_t>(L.max_slots) * Hkv * kPlanWarps * sizeof(int));
     const size_t rows = static_cast<size_t>(L.max_slots) * Hkv * 256;
     L.o = L.ml + plan_up(rows * 2 * sizeof(float));
     L.total = L.o + plan_up(rows * D * sizeof(float));
