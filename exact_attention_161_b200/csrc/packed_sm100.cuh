@@ -442,59 +442,72 @@ __device__ __noinline__ void join_parts(const PackedParams& p, int g, int q_row,
     constexpr int PER = D / 32;  // columns of a lane
     const int lane = threadIdx.x & 31;
     if (tok * p.G <= quad * 32) return;  // none of its rows is live
-    __threadfence();  // this lane's states before the count
+    // the warp's states before the count, the count before the other parts' states
     __syncwarp();
     int last = 0;
     if (lane == 0)
-        last = atomicAdd(p.count + (static_cast<size_t>(slot) * p.Hkv + g) * kPlanWarps + wg * 4 + quad, 1) == parts - 1;
+        last = ptx::atomic_add_acq_rel(p.count + (static_cast<size_t>(slot) * p.Hkv + g) * kPlanWarps + wg * 4 + quad, 1) == parts - 1;
     if (!__shfl_sync(0xffffffffu, last, 0)) return;
-    __threadfence();  // the count before the other parts' states
     const size_t step = static_cast<size_t>(p.Hkv) * 256;  // rows from one part's state to the next
     const int rows = min(32, tok * p.G - quad * 32);  // live rows of this warp
     const size_t row0 = (static_cast<size_t>(slot) * p.Hkv + g) * 256 + wg * 128 + quad * 32;
     const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + row0;
-    float M = -INFINITY, inv = 0.f;  // of row `lane`
-    if (lane < rows) {
-        float L = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(ml + lane + i * step).x);
-#pragma unroll 8
-        for (int i = 0; i < parts; ++i) {
-            const float2 s = __ldcg(ml + lane + i * step);
-            L = fmaf(s.x == -INFINITY ? 0.f : ptx::ex2(s.x - M), s.y, L);  // -inf: none of the row's keys, and no output
-        }
-        inv = L > 0.f ? 1.f / L : 0.f;
+    constexpr int B = 8;  // parts at a time
+    const int my_row = min(lane, rows - 1);
+    float M = -INFINITY, L = 0.f;  // of row `lane`
+    for (int base = 0; base < parts; base += B) {
+        float2 x[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j) x[j] = __ldcg(ml + my_row + min(base + j, parts - 1) * step);
+        float top = M;
+#pragma unroll
+        for (int j = 0; j < B; ++j) top = fmaxf(top, x[j].x);
+        L *= M == -INFINITY ? 0.f : ptx::ex2(M - top);
+        M = top;
+#pragma unroll
+        for (int j = 0; j < B; ++j)  // -inf: none of the row's keys, and no output
+            if (base + j < parts && x[j].x != -INFINITY) L = fmaf(ptx::ex2(x[j].x - M), x[j].y, L);
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    if (lane < rows && p.lse != nullptr) {
         const int r = quad * 32 + lane, t = r / p.G, h = g * p.G + r - t * p.G;
         const size_t row = static_cast<size_t>(q_row) + t;
-        if (p.lse != nullptr) p.lse[row * p.lse_t + h * p.lse_h] = L > 0.f ? (M + ptx::lg2(L)) * kLn2 : -INFINITY;
+        p.lse[row * p.lse_t + h * p.lse_h] = L > 0.f ? (M + ptx::lg2(L)) * kLn2 : -INFINITY;
     }
-    constexpr int R = 4;         // rows at a time
+    constexpr int R = 4, P = 4;  // rows and parts at a time
     for (int r0 = 0; r0 < rows; r0 += R) {
-        float acc[R][PER], Mr[R];
+        float acc[R][PER];
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            Mr[j] = __shfl_sync(0xffffffffu, M, min(r0 + j, rows - 1));
+        for (int j = 0; j < R; ++j)
 #pragma unroll
             for (int c = 0; c < PER; ++c) acc[j][c] = 0.f;
-        }
-#pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
+        for (int base = 0; base < parts; base += P) {
+            float w[P], v[P][R][PER];  // w: of row `lane`
 #pragma unroll
-            for (int j = 0; j < R; ++j) {
-                const size_t at = min(r0 + j, rows - 1) + i * step;
-                const float m = __ldcg(ml + at).x;
-                const float* o = p.ws_o + (row0 + at) * D + lane * PER;
-                float v[PER];
-                if constexpr (PER == 4) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4*>(o));
-                    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-                } else {
-                    const float2 x = __ldcg(reinterpret_cast<const float2*>(o));
-                    v[0] = x.x; v[1] = x.y;
+            for (int i = 0; i < P; ++i) {
+                const size_t part = min(base + i, parts - 1) * step;
+                w[i] = __ldcg(ml + my_row + part).x;
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    const float* o = p.ws_o + (row0 + min(r0 + j, rows - 1) + part) * D + lane * PER;
+                    if constexpr (PER == 4) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(o));
+                        v[i][j][0] = y.x; v[i][j][1] = y.y; v[i][j][2] = y.z; v[i][j][3] = y.w;
+                    } else {
+                        const float2 y = __ldcg(reinterpret_cast<const float2*>(o));
+                        v[i][j][0] = y.x; v[i][j][1] = y.y;
+                    }
                 }
-                const float w = ptx::ex2(m - Mr[j]);
+            }
 #pragma unroll
-                for (int c = 0; c < PER; ++c) acc[j][c] = m == -INFINITY ? acc[j][c] : fmaf(w, v[c], acc[j][c]);
+            for (int i = 0; i < P; ++i) {
+                w[i] = base + i < parts && w[i] != -INFINITY ? ptx::ex2(w[i] - M) : 0.f;
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    const float wr = __shfl_sync(0xffffffffu, w[i], min(r0 + j, rows - 1));
+#pragma unroll
+                    for (int c = 0; c < PER; ++c) acc[j][c] = wr > 0.f ? fmaf(wr, v[i][j][c], acc[j][c]) : acc[j][c];
+                }
             }
         }
 #pragma unroll
@@ -515,7 +528,9 @@ __device__ __noinline__ void join_parts(const PackedParams& p, int g, int q_row,
 template <int D>
 struct PackedCfg {
     static constexpr bool kSplitP = D == 64;
-    static constexpr int THREADS = FwdCfg<D>::THREADS + (kSplitP ? 32 : 0);  // a second MMA issuer
+    // beside the softmax warps: producer of Q and K, MMA issuer, (kSplitP) issuer of the outputs, producer of V
+    static constexpr int V_WARP = kSplitP ? 11 : 10;
+    static constexpr int THREADS = (V_WARP + 1) * 32;
     static constexpr int BAR_BYTES = 2048;
     // tiles, barriers, and the gap in front of the tiles' 1024-byte boundary
     static constexpr int SMEM_BYTES = FwdCfg<D>::SMEM_TILES * FwdCfg<D>::TILE_BYTES + BAR_BYTES + 1024;
@@ -531,7 +546,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
     constexpr int kPages = C::BN / kPageSize;  // pages of a key tile
     // At D = 64 Tensor Memory has room for P beside S: see the MMA issuer.
     constexpr bool kSplitP = PackedCfg<D>::kSplitP;
-    constexpr int kConsumers = kSplitP ? 10 : 9;  // warps that read the work ring: softmax and MMA issuers
+    constexpr int kConsumers = kSplitP ? 11 : 10;  // warps that read the work ring: all but the producer of Q and K
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
@@ -591,12 +606,47 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
     // TMEM columns of P: over the first half of S, or behind the accumulators
     auto tmem_p = [](int i) { return kSplitP ? 256u + 2u * D + 64u * i : C::tmem_s(i); };
 
+    // Key tile of a step, loaded by a whole warp: lane 0 expects the bytes; a packed tile's boxes are issued
+    // by lane 0, those of a paged tile by the lane that looked the page up (`page`; -1: none, read as zeros
+    // by a box outside the tensor, so that what its memory holds cannot reach a product).
+    auto load_tile = [&](const PackedWork& x, const CUtensorMap* tm, uint8_t* dst, uint64_t* full, int jt, int page, bool drop) {
+        if constexpr (kPaged) {
+            const int pages = min(kPages, (x.kv_len + kPageSize - 1) / kPageSize - jt * kPages);
+            const int z = page >= 0 && page < p.num_pages ? page * p.Hkv + x.g : -1;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(full, pages * kPageSize * C::ROW_BYTES);
+            __syncwarp();
+            if (lane < pages && !drop) {
+#pragma unroll
+                for (int r = 0; r < C::NREG; ++r)
+                    ptx::tma_load_3d(dst + r * C::REGION_BYTES + lane * kPageSize * 128, tm, full, r * 64, 0, z);
+            }
+        } else if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(full, C::TILE_BYTES);
+            if (!drop) {
+#pragma unroll
+                for (int r = 0; r < C::NREG; ++r)
+                    ptx::tma_load_3d(dst + r * C::REGION_BYTES, tm, full, r * 64, x.g, x.kv + jt * C::BN);
+            }
+        }
+    };
+    // lane i of a paged tile: page i of the tile of step u. Pages before the window of the item's first
+    // token may have been given back: they are not looked up.
+    auto look_up = [&](const PackedWork& x, int u) {
+        if (!kPaged || lane >= kPages || u >= x.T) return -1;
+        const int pg = (x.J0 + x.tile(u)) * kPages + lane;
+        const int first_page = p.window > 0 ? max(0, x.pos0 - p.window + 1) / kPageSize : 0;
+        if (pg < first_page || pg >= (x.kv_len + kPageSize - 1) / kPageSize) return -1;
+        const int page = p.block_table[static_cast<size_t>(x.kv) * p.max_blocks + pg];
+        if (page < 0 || page >= p.num_pages) raise_status(kStatusBadPage);
+        return page;
+    };
+
     if (warp == C::PRODUCER_WARP) {
         // ------------------------------------------------------------------ TMA producer
-        // The whole warp walks the items. Lane 0 expects the bytes; the boxes of a packed tile are
-        // issued by lane 0, those of a paged tile by the lane that looked the page up.
+        // Decodes the items into the work ring and loads Q and K.
         int kq[2] = {0, 0};
-        int g = 0, k_issued = 0, v_issued = 0;
+        int sk = 0, issued = 0;
+        uint32_t free_par = 1;  // (a fresh barrier passes parity 1)
         bool ok = true;
         int4 rec_lo{}, rec_hi{};  // the next item's record, loaded one item ahead
         auto load_record = [&](int it) {
@@ -614,6 +664,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 bar->work[ws] = x;
                 ptx::mbar_arrive(&bar->work_full[ws]);
             }
+            int page = look_up(x, 0);
             next = item_of_round(++rnd, blockIdx.x, gridDim.x);
             load_record(next);
             for (int i = 0; i < 2 && ok; ++i) {
@@ -628,67 +679,17 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 }
                 ++kq[i];
             }
-            const int32_t* bt = kPaged ? p.block_table + static_cast<size_t>(x.kv) * p.max_blocks : nullptr;
-            const int seq_pages = kPaged ? (x.kv_len + kPageSize - 1) / kPageSize : 0;
-            // pages before the window of the item's first token may have been given back: not looked up
-            const int first_page = p.window > 0 ? max(0, x.pos0 - p.window + 1) / kPageSize : 0;
-            // lane i of a paged tile: page i of the next tile, looked up one tile ahead
-            int page = 0;
-            auto look_up = [&](int u) {
-                const int pg = (x.J0 + x.tile(u)) * kPages + lane;
-                return (lane < kPages && u < x.T && pg < seq_pages && pg >= first_page) ? bt[pg] : -1;
-            };
-            if constexpr (kPaged) page = look_up(0);
-            for (int u = 0; u < x.T && ok; ++u, ++g) {
-                const int jt = x.J0 + x.tile(u), k0 = jt * C::BN;
-                const int sk = g % NK, sv = g % NV;
-                if (g >= NK && !ptx::mbar_wait_warp(&bar->k_empty[sk], ((g / NK) - 1) & 1, abort_flag)) { ok = false; break; }
-                const bool drop = p.debug_drop_copy && g == 0 && blockIdx.x == 0;
-                int z = 0, pages = 0;
-                if constexpr (kPaged) {
-                    pages = min(kPages, seq_pages - jt * kPages);
-                    // a page that is invalid (flagged) or before the window is read as zeros, by a box
-                    // outside the tensor: what its memory holds cannot reach a product
-                    const bool valid = page >= 0 && page < p.num_pages;
-                    if (lane < pages && !valid && jt * kPages + lane >= first_page) raise_status(kStatusBadPage);
-                    z = valid ? page * p.Hkv + x.g : -1;
-                    page = look_up(u + 1);
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(&bar->k_full[sk], pages * kPageSize * C::ROW_BYTES);
-                    __syncwarp();
-                    if (lane < pages && !drop) {
-#pragma unroll
-                        for (int r = 0; r < C::NREG; ++r)
-                            ptx::tma_load_3d(sK + sk * C::TILE_BYTES + r * C::REGION_BYTES + lane * kPageSize * 128, &tm_k,
-                                             &bar->k_full[sk], r * 64, 0, z);
-                    }
-                } else if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(&bar->k_full[sk], C::TILE_BYTES);
-                    if (!drop) {
-#pragma unroll
-                        for (int r = 0; r < C::NREG; ++r)
-                            ptx::tma_load_3d(sK + sk * C::TILE_BYTES + r * C::REGION_BYTES, &tm_k, &bar->k_full[sk], r * 64,
-                                             x.g, x.kv + k0);
-                    }
+            for (int u = 0; u < x.T && ok; ++u) {
+                if (!ptx::mbar_wait_warp(&bar->k_empty[sk], free_par, abort_flag)) { ok = false; break; }
+                const int now = page;
+                page = look_up(x, u + 1);  // one tile ahead
+                load_tile(x, &tm_k, sK + sk * C::TILE_BYTES, &bar->k_full[sk], x.J0 + x.tile(u), now,
+                          p.debug_drop_copy && issued == 0 && blockIdx.x == 0);
+                ++issued;
+                if (++sk == NK) {
+                    sk = 0;
+                    free_par ^= 1;
                 }
-                k_issued = g + 1;
-                if (g >= NV && !ptx::mbar_wait_warp(&bar->v_empty[sv], ((g / NV) - 1) & 1, abort_flag)) { ok = false; break; }
-                if constexpr (kPaged) {
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(&bar->v_full[sv], pages * kPageSize * C::ROW_BYTES);
-                    __syncwarp();
-                    if (lane < pages) {
-#pragma unroll
-                        for (int r = 0; r < C::NREG; ++r)
-                            ptx::tma_load_3d(sV + sv * C::TILE_BYTES + r * C::REGION_BYTES + lane * kPageSize * 128, &tm_v,
-                                             &bar->v_full[sv], r * 64, 0, z);
-                    }
-                } else if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(&bar->v_full[sv], C::TILE_BYTES);
-#pragma unroll
-                    for (int r = 0; r < C::NREG; ++r)
-                        ptx::tma_load_3d(sV + sv * C::TILE_BYTES + r * C::REGION_BYTES, &tm_v, &bar->v_full[sv], r * 64, x.g,
-                                         x.kv + k0);
-                }
-                v_issued = g + 1;
             }
         }
         if (!ok && lane == 0) {
@@ -698,8 +699,40 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
             volatile int never = 0;
             for (int i = 0; i < 2; ++i)
                 if (kq[i] > 0) ptx::mbar_wait(&bar->q_loaded[i], (kq[i] - 1) & 1, &never);
-            for (int u = max(0, k_issued - NK); u < k_issued; ++u) ptx::mbar_wait(&bar->k_full[u % NK], (u / NK) & 1, &never);
-            for (int u = max(0, v_issued - NV); u < v_issued; ++u) ptx::mbar_wait(&bar->v_full[u % NV], (u / NV) & 1, &never);
+            for (int u = max(0, issued - NK); u < issued; ++u) ptx::mbar_wait(&bar->k_full[u % NK], (u / NK) & 1, &never);
+        }
+        __syncwarp();
+    } else if (warp == PackedCfg<D>::V_WARP) {
+        // ------------------------------------------------------------------ producer of V
+        // A warp of its own: the 16 boxes of a paged 128-key tile take 1,200 clocks to issue at D = 128,
+        // and one warp issuing K and V bounded single tokens at 2,900 clocks a tile.
+        int sv = 0, issued = 0;
+        uint32_t free_par = 1;
+        bool ok = true;
+        for (int rnd = 0, it = blockIdx.x; ok && it < n_items; it = item_of_round(++rnd, blockIdx.x, gridDim.x)) {
+            const int ws = rnd % kWorkRing;
+            if (!ptx::mbar_wait_warp(&bar->work_full[ws], (rnd / kWorkRing) & 1, abort_flag)) { ok = false; break; }
+            const PackedWork x = bar->work[ws];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bar->work_empty[ws]);
+            int page = look_up(x, 0);
+            for (int u = 0; u < x.T && ok; ++u) {
+                if (!ptx::mbar_wait_warp(&bar->v_empty[sv], free_par, abort_flag)) { ok = false; break; }
+                const int now = page;
+                page = look_up(x, u + 1);
+                load_tile(x, &tm_v, sV + sv * C::TILE_BYTES, &bar->v_full[sv], x.J0 + x.tile(u), now, false);
+                ++issued;
+                if (++sv == NV) {
+                    sv = 0;
+                    free_par ^= 1;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            *abort_flag = 1;
+            raise_status(kStatusTimeout);
+            volatile int never = 0;  // as above
+            for (int u = max(0, issued - NV); u < issued; ++u) ptx::mbar_wait(&bar->v_full[u % NV], (u / NV) & 1, &never);
         }
         __syncwarp();
     } else if (warp >= C::MMA_WARP) {

@@ -456,6 +456,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+// Adds to a counter in global memory; what the thread (and threads it has synchronised with) wrote before
+// is visible to whoever reads the counter by this function afterwards.
+__device__ __forceinline__ int atomic_add_acq_rel(int* p, int x) {
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(x) : "memory");
+    return old;
+}
 // 32 bytes to a 32-byte aligned global address (sm_100a).
 __device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
