@@ -823,8 +823,10 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bar->work_empty[ws]);
-            for (int u = kSplitP ? 0 : -1; ok && u < T; ++u) {
-                const int us = kSplitP ? u : u + 1;  // the key tile whose scores this step computes
+            // the scores run ahead of the outputs by one key tile of the same query tile
+            const int ahead = kSplitP ? 0 : half > 0 ? 2 : 1;
+            for (int u = -ahead; ok && u < T; ++u) {
+                const int us = u + ahead;  // the step whose scores are due
                 if (outputs && u >= 0) {
                     if (!ptx::mbar_wait_warp(&bar->v_full[sv], pv, abort_flag)) { ok = false; break; }
                 }
