@@ -1097,20 +1097,20 @@ attn_status attn_rope_axes(const void* q, void* q_out, const void* k, void* k_ou
     int dev = 0, sms = 148;
     CUDA_TRY(cudaGetDevice(&dev));
     CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    // tokens a CTA rotates at a time: enough for four items per thread, but no fewer than two CTAs per
-    // SM while there are tokens for them
-    const int per_token = (Hq + Hk) * (D / 16);
-    int group = 1024 / per_token;
-    group = group < 1 ? 1 : group > 16 ? 16 : group;
-    while (group > 1 && T / group < 2 * sms) group /= 2;
-    p.group = group;
-    const long long want = (static_cast<long long>(T) + group - 1) / group;
-    const unsigned grid = static_cast<unsigned>(want < 8LL * sms ? want : 8LL * sms);
+    // A warp takes a token's heads, or fewer where that leaves fewer than 16 warps per SM, down to those that
+    // its lanes hold at once.
+    const int H = Hq + Hk, at_once = 32 / (D / 16);
+    int share = 1;
+    while (static_cast<long long>(T) * share < 16LL * sms && (H + 2 * share - 1) / (2 * share) >= at_once) share *= 2;
+    p.per_share = (H + share - 1) / share;
+    p.share = (H + p.per_share - 1) / p.per_share;
+    const long long want = (static_cast<long long>(T) * p.share + 3) / 4;
+    const unsigned grid = static_cast<unsigned>(want < 32LL * sms ? want : 32LL * sms);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (D == 64)
-        attn::rope_axes_kernel<64><<<grid, 256, 0, s>>>(p);
+        attn::rope_axes_kernel<64><<<grid, 128, 0, s>>>(p);
     else
-        attn::rope_axes_kernel<128><<<grid, 256, 0, s>>>(p);
+        attn::rope_axes_kernel<128><<<grid, 128, 0, s>>>(p);
     CUDA_TRY(cudaGetLastError());
     return ATTN_OK;
 }
