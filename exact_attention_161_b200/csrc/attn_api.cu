@@ -760,11 +760,9 @@ attn_status launch_packed_bwd(const void* q, const void* k, const void* v, long 
     if ((st = make_map_2d_f32(&tdq, p.dqacc, D, static_cast<uint64_t>(L.max_tiles) * Hq * 128)) != ATTN_OK) return st;
     if ((st = ensure_smem(attn::attn_bwd_kernel<D, true>, C::SMEM_BYTES, dev)) != ATTN_OK) return st;
     cudaLaunchAttribute attr[1];
-    // rows a block of the prep pass and of the dq pass takes at a time
-    const long long rows = L.max_tiles * Hq * 128, prep = (rows * (D / 8) + 255) / 256;
-    const unsigned pass_grid = static_cast<unsigned>(prep < 16LL * sms ? prep : 16LL * sms);
+    const unsigned pass_grid = static_cast<unsigned>(L.max_tiles * Hq);  // the device knows how many tiles there are
     cudaLaunchConfig_t lc = dependent_launch(pass_grid, 256, 0, stream, attr);
-    CUDA_TRY(cudaLaunchKernelEx(&lc, attn::bwd_prep_kernel<D, true>, static_cast<const attn::BwdParams>(p)));
+    CUDA_TRY(cudaLaunchKernelEx(&lc, attn::bwd_prep_packed_kernel<D>, static_cast<const attn::BwdParams>(p)));
     lc = dependent_launch(static_cast<unsigned>(L.max_tiles * Hkv), C::THREADS, C::SMEM_BYTES, stream, attr);
     CUDA_TRY(cudaLaunchKernelEx(&lc, attn::attn_bwd_kernel<D, true>, tq, tk, tv, tdo, tdq, p));
     lc = dependent_launch(pass_grid, 256, 0, stream, attr);

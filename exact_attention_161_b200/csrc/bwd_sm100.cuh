@@ -58,50 +58,23 @@ struct BwdParams {
 // them, and the row's fp32 dq sums set to zero. D/8 lanes share a row (16-byte loads), grid-stride
 // over all padded rows; rows past N get (-inf, 0) so that their recomputed probabilities are
 // exactly 0.
-// kPacked: the rows of a tile are walked token by token (the heads of a token lie side by side).
-template <int D, bool kPacked = false>
+template <int D>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const BwdParams p) {
     constexpr int LPR = D / 8;     // lanes per row
     constexpr int RPW = 32 / LPR;  // rows per warp and pass
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-    if constexpr (kPacked) {
-        ptx::grid_launch_dependents();
-        ptx::grid_dependency_wait();  // the plan
-    }
     const long long npad = static_cast<long long>(p.ntiles) * 128;
-    const long long rows = kPacked ? static_cast<long long>(p.header->n_items) * 128 * p.Hq
-                                   : static_cast<long long>(p.B) * p.Hq * npad;
+    const long long rows = static_cast<long long>(p.B) * p.Hq * npad;
     const long long nwarps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
     for (long long base = (static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * RPW;
          base < rows; base += nwarps * RPW) {
         const long long row = base + sub;
-        bool valid;
-        size_t off = 0, lse_at = 0, zrow = static_cast<size_t>(row), vec_at;
-        if constexpr (kPacked) {
-            const long long tr = row / p.Hq;  // padded token: tile * 128 + i
-            const int h = static_cast<int>(row - tr * p.Hq), i = static_cast<int>(tr & 127);
-            valid = false;
-            if (row < rows) {
-                const PackedTile t = p.tiles[tr >> 7];
-                valid = t.t * 128 + i < t.n;
-                const size_t token = static_cast<size_t>(t.row0) + t.t * 128 + i;
-                off = (token * p.Hq + h) * D;
-                lse_at = static_cast<size_t>(h) * p.T + token;
-            }
-            const size_t th = static_cast<size_t>(tr >> 7) * p.Hq + h;
-            zrow = th * 128 + i;
-            vec_at = th * 256 + i;
-        } else {
-            const long long bh = row / npad;
-            const int i = static_cast<int>(row - bh * npad);
-            valid = row < rows && i < p.N;
-            off = (static_cast<size_t>(bh) * p.N + i) * D;
-            lse_at = static_cast<size_t>(bh) * p.N + i;
-            vec_at = (static_cast<size_t>(bh) * p.ntiles + i / 128) * 256 + (i & 127);
-        }
+        const long long bh = row / npad;
+        const int i = static_cast<int>(row - bh * npad);
+        const bool valid = row < rows && i < p.N;
         float acc = 0.f;
         if (valid) {
-            off += l * 8;
+            const size_t off = (static_cast<size_t>(bh) * p.N + i) * D + l * 8;
             const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.o + off));
             const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.dout + off));
             const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
@@ -112,16 +85,63 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const BwdParams p) {
             }
         }
         if (row < rows) {
-            float4* z = reinterpret_cast<float4*>(p.dqacc + zrow * D + l * 8);
+            float4* z = reinterpret_cast<float4*>(p.dqacc + static_cast<size_t>(row) * D + l * 8);
             z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
             z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int m = LPR / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
         if (row < rows && l == 0) {
-            float* v = p.vec + vec_at;
-            v[0] = valid ? -p.lse[lse_at] * kLog2e : -INFINITY;
+            float* v = p.vec + (static_cast<size_t>(bh) * p.ntiles + i / 128) * 256 + (i & 127);
+            v[0] = valid ? -p.lse[static_cast<size_t>(bh) * p.N + i] * kLog2e : -INFINITY;
             v[128] = valid ? -acc : 0.f;
+        }
+    }
+}
+
+// The same for packed sequences, a block per (tile, query head). All of a thread's loads are issued
+// before the first is used.
+template <int D>
+__global__ void __launch_bounds__(256) bwd_prep_packed_kernel(const BwdParams p) {
+    constexpr int LPR = D / 8, RPP = 256 / LPR, PASSES = 128 / RPP;  // lanes per row, rows per pass
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();  // the plan
+    const int tile = static_cast<int>(blockIdx.x / p.Hq), h = static_cast<int>(blockIdx.x - static_cast<unsigned>(tile) * p.Hq);
+    if (tile >= p.header->n_items) return;
+    const PackedTile t = p.tiles[tile];
+    const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+    const int rows = min(128, t.n - t.t * 128);
+    const size_t token0 = static_cast<size_t>(t.row0) + t.t * 128;
+    uint4 a[PASSES], b[PASSES];
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+        a[k] = b[k] = make_uint4(0, 0, 0, 0);
+        const int i = r0 + k * RPP;
+        if (i >= rows) continue;
+        const size_t off = ((token0 + i) * p.Hq + h) * D + l * 8;
+        a[k] = __ldg(reinterpret_cast<const uint4*>(p.o + off));
+        b[k] = __ldg(reinterpret_cast<const uint4*>(p.dout + off));
+    }
+    const size_t th = blockIdx.x;
+    float4* z = reinterpret_cast<float4*>(p.dqacc + th * 128 * D) + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 128 * D / 4 / 256; ++k) z[k * 256] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+        const int i = r0 + k * RPP;
+        const uint32_t aw[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, bw[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+        float acc = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc = fmaf(ptx::bf16lo_to_f32(aw[e]), ptx::bf16lo_to_f32(bw[e]), acc);
+            acc = fmaf(ptx::bf16hi_to_f32(aw[e]), ptx::bf16hi_to_f32(bw[e]), acc);
+        }
+#pragma unroll
+        for (int m = LPR / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+        if (l == 0) {
+            float* v = p.vec + th * 256 + i;
+            v[0] = i < rows ? -p.lse[static_cast<size_t>(h) * p.T + token0 + i] * kLog2e : -INFINITY;
+            v[128] = i < rows ? -acc : 0.f;
         }
     }
 }
@@ -726,28 +746,33 @@ __global__ void __launch_bounds__(256) bwd_dq_store_kernel(const BwdParams p) {
     }
 }
 
-// The same for packed sequences: the rows of a tile token by token, stored dq_stride elements apart.
+// The same for packed sequences, a block per (tile, query head), rows dq_stride elements apart.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_dq_store_packed_kernel(const BwdParams p) {
+    constexpr int LPR = D / 8, RPP = 256 / LPR, PASSES = 128 / RPP;
     ptx::grid_dependency_wait();
-    constexpr int CPR = D / 8;
-    const long long total = static_cast<long long>(p.header->n_items) * 128 * p.Hq * CPR;
-    for (long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; idx < total;
-         idx += static_cast<long long>(gridDim.x) * blockDim.x) {
-        const long long row = idx / CPR;
-        const int c0 = static_cast<int>(idx - row * CPR) * 8;
-        const long long tr = row / p.Hq;
-        const int h = static_cast<int>(row - tr * p.Hq), i = static_cast<int>(tr & 127);
-        const PackedTile t = p.tiles[tr >> 7];
-        if (t.t * 128 + i >= t.n) continue;
-        const float4* src =
-            reinterpret_cast<const float4*>(p.dqacc + ((static_cast<size_t>(tr >> 7) * p.Hq + h) * 128 + i) * D + c0);
-        const float4 a = src[0], c = src[1];
-        const size_t token = static_cast<size_t>(t.row0) + t.t * 128 + i;
-        *reinterpret_cast<uint4*>(p.dq + token * p.dq_stride + h * D + c0) =
-            make_uint4(ptx::pack_bf16x2(a.x * p.scale, a.y * p.scale), ptx::pack_bf16x2(a.z * p.scale, a.w * p.scale),
-                       ptx::pack_bf16x2(c.x * p.scale, c.y * p.scale), ptx::pack_bf16x2(c.z * p.scale, c.w * p.scale));
+    const int tile = static_cast<int>(blockIdx.x / p.Hq), h = static_cast<int>(blockIdx.x - static_cast<unsigned>(tile) * p.Hq);
+    if (tile >= p.header->n_items) return;
+    const PackedTile t = p.tiles[tile];
+    const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+    const int rows = min(128, t.n - t.t * 128);
+    const float* src = p.dqacc + (static_cast<size_t>(blockIdx.x) * 128 + r0) * D + l * 8;
+    float4 a[PASSES], c[PASSES];
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+        const float4* x = reinterpret_cast<const float4*>(src + static_cast<size_t>(k) * RPP * D);
+        if (r0 + k * RPP < rows) {
+            a[k] = __ldcs(x);
+            c[k] = __ldcs(x + 1);
+        }
     }
+    __nv_bfloat16* dst = p.dq + (static_cast<size_t>(t.row0) + t.t * 128 + r0) * p.dq_stride + h * D + l * 8;
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k)
+        if (r0 + k * RPP < rows)
+            *reinterpret_cast<uint4*>(dst + static_cast<long long>(k) * RPP * p.dq_stride) =
+                make_uint4(ptx::pack_bf16x2(a[k].x * p.scale, a[k].y * p.scale), ptx::pack_bf16x2(a[k].z * p.scale, a[k].w * p.scale),
+                           ptx::pack_bf16x2(c[k].x * p.scale, c[k].y * p.scale), ptx::pack_bf16x2(c[k].z * p.scale, c[k].w * p.scale));
 }
 
 }  // namespace attn
