@@ -479,12 +479,13 @@ def attn_rope_axes(q, k, positions, sections, interleave_axes=False, per_axis_fr
     if q.dim() != 3 or k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]):
         raise ValueError("q must be [T, Hq, D] and k [T, Hk, D]")
     T, Hq, D = q.shape
-    n_axes, dev = len(sections), _device_of(q)
+    n_axes = len(sections)
     if positions.shape != (n_axes, T):
         raise ValueError("positions must be [len(sections), T]")
     for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
         if t is not None and (like is None or t.shape != like.shape):
             raise ValueError("%s has another shape than its input" % name)
+    dev = _device_of(q)
 
     def call(st):
         yq = torch.empty((T, Hq, D), dtype=_BF16, device=q.device) if q_out is None else q_out

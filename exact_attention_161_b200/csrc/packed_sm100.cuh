@@ -11,7 +11,8 @@
 //     128-byte region. Short sequences and single tokens then fill G times more of a tile, and a
 //     K/V tile is read once for the whole group. (G that does not divide 128 leaves 128 - G TT rows
 //     of every tile unused: 2 for G = 3, 8 for G = 5.)
-//   Items. The list of plan.cuh, walked by one persistent CTA per SM, longest items first.
+//   Items. The list of plan.cuh, longest items first; one persistent CTA per SM takes the next when it is
+//     nearly done with one.
 //   Parts. A block whose keys were cut into parts writes fp32 partial states; of each group of 32 rows,
 //     the warp that finishes last joins them in ascending order.
 //   Sides. A block of at most TT tokens has one query tile. Both softmax warpgroups work on it, each with a
@@ -85,9 +86,9 @@ __device__ __forceinline__ int plan_scan(int x, int* warp_sums, int& total) {
 // long enough for it), the list. Runs in a few microseconds; what it costs is the latency of its steps,
 // not the number of blocks.
 //
-// Whether to cut: CTA c takes items c, 2 G - 1 - c, ... of the descending list, so no CTA gets more key
-// tiles than the sum of every G-th item. Blocks are cut when that sum with all parts within the limit,
-// plus the cost of joining, is below the sum without.
+// Whether to cut: taken in turns from the descending list, no CTA of G gets more than the sum of every
+// G-th item. Blocks are cut when that sum with all parts within the limit, plus the cost of joining, is
+// below the sum without.
 template <bool kBwd>
 __device__ void build_plan(const PlanParams& p) {
     __shared__ int s_hist[kPlanBuckets];
@@ -135,7 +136,7 @@ __device__ void build_plan(const PlanParams& p) {
     __syncthreads();
 
     struct Block {
-        int s, first, n, tiles, kv_len;  // sequence, first token and tokens of the block, its tiles, keys
+        int s, first, n, tiles, cost, kv_len;  // sequence, first token and tokens of the block, its tiles, keys
     };
     auto block_of = [&](int b) {
         int lo = 0, hi = p.S - 1;  // the last sequence whose first block is <= b (empty ones never are the last)
@@ -154,7 +155,7 @@ __device__ void build_plan(const PlanParams& p) {
         if constexpr (kBwd) {
             int ib, ie;
             query_tiles(b - pre[lo], n, p.causal, p.window, ib, ie);
-            x.tiles = max(0, ie - ib);
+            x.tiles = x.cost = max(0, ie - ib);
             x.kv_len = n;
         } else {
             int len = n;
@@ -165,6 +166,7 @@ __device__ void build_plan(const PlanParams& p) {
             x.kv_len = len;
             const int pos = len - n + x.first;
             x.tiles = len < 0 ? 0 : key_tiles(pos, pos + x.n - 1, len, p.causal, p.window).n;
+            x.cost = plan_cost(x.tiles, x.n <= p.TT);
         }
         return x;
     };
@@ -176,8 +178,8 @@ __device__ void build_plan(const PlanParams& p) {
     int most = 1;
     for (int b = tid; b < n_blocks; b += kPlanThreads) {
         const Block x = get(b);
-        sum += x.tiles;
-        most = max(most, x.tiles);
+        sum += x.cost;
+        most = max(most, x.cost);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -189,8 +191,9 @@ __device__ void build_plan(const PlanParams& p) {
     __syncthreads();
     const int limit = kBwd ? 0x3fffffff : plan_limit(static_cast<long long>(s_sum), p.Hkv);
     const int longest = s_max;
-    auto bucket = [&](int tiles) {
-        return kPlanBuckets - 1 - static_cast<int>(static_cast<long long>(tiles) * (kPlanBuckets - 1) / longest);
+    auto bucket = [&](const Block& x, int tiles) {  // of an item of block x
+        const long long cost = kBwd ? tiles : plan_cost(tiles, x.n <= p.TT);
+        return kPlanBuckets - 1 - static_cast<int>(cost * (kPlanBuckets - 1) / longest);
     };
     int n_items = 0;
     bool cut = false;
@@ -200,9 +203,9 @@ __device__ void build_plan(const PlanParams& p) {
         __syncthreads();
         for (int b = tid; b < n_blocks; b += kPlanThreads) {
             const Block x = get(b);
-            const int parts = with_parts ? plan_parts(x.tiles, limit) : 1, q = x.tiles / parts, r = x.tiles % parts;
-            if (r > 0) atomicAdd(&s_hist[bucket(q + 1)], r);
-            atomicAdd(&s_hist[bucket(q)], parts - r);
+            const int parts = with_parts ? plan_parts(x.cost, limit) : 1, q = x.tiles / parts, r = x.tiles % parts;
+            if (r > 0) atomicAdd(&s_hist[bucket(x, q + 1)], r);
+            atomicAdd(&s_hist[bucket(x, q)], parts - r);
         }
         __syncthreads();
         const int mine_n = s_hist[tid];
@@ -243,9 +246,9 @@ __device__ void build_plan(const PlanParams& p) {
             t.base = pre[x.s];
             t.t = b - t.base;
             p.tiles[b] = t;
-            p.order[atomicAdd(&s_hist[bucket(x.tiles)], 1)] = b;
+            p.order[atomicAdd(&s_hist[bucket(x, x.tiles)], 1)] = b;
         } else {
-            const int parts = cut ? plan_parts(x.tiles, limit) : 1;
+            const int parts = cut ? plan_parts(x.cost, limit) : 1;
             const int row0 = p.cu[x.s];
             const int n = p.cu[x.s + 1] - row0;
             PackedItem it;
@@ -266,7 +269,7 @@ __device__ void build_plan(const PlanParams& p) {
                 it.jb = jb + b0;
                 it.n_tiles = b1 - b0;
                 it.meta = make_meta(x.n, i, parts);
-                p.items[atomicAdd(&s_hist[bucket(it.n_tiles)], 1)] = it;
+                p.items[atomicAdd(&s_hist[bucket(x, it.n_tiles)], 1)] = it;
             }
         }
     }
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PlanPar
 }
 
 struct PackedParams {
-    const PlanHeader* header;
+    PlanHeader* header;
     const PackedItem* items;
     const int32_t* block_table;  // paged
     __nv_bfloat16* o;            // [T, Hq, D]
@@ -655,18 +658,29 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
             rec_lo = rec[0];
             rec_hi = rec[1];
         };
-        load_record(blockIdx.x);
-        for (int rnd = 0, it = blockIdx.x, next; ok && it < n_items; it = next) {
-            const PackedWork x = decode_item(p, rec_lo, rec_hi, it % p.Hkv);
+        int it = blockIdx.x;
+        load_record(it);
+        for (int rnd = 0; ok; ++rnd) {
+            PackedWork x = decode_item(p, rec_lo, rec_hi, it % p.Hkv);
+            if (it >= n_items) x.T = -1;  // the end, for every reader of the ring
             const int ws = rnd % kWorkRing;
             if (rnd >= kWorkRing && !ptx::mbar_wait_warp(&bar->work_empty[ws], (rnd / kWorkRing - 1) & 1, abort_flag)) { ok = false; break; }
             if (lane == 0) {
                 bar->work[ws] = x;
                 ptx::mbar_arrive(&bar->work_full[ws]);
             }
+            if (x.T < 0) break;
             int page = look_up(x, 0);
-            next = item_of_round(++rnd, blockIdx.x, gridDim.x);
-            load_record(next);
+            // the next item, taken a few tiles before this one's end: early enough to hide the latency, late
+            // enough that CTAs with long items take fewer
+            const int take = max(0, x.T - 4);
+            auto take_next = [&]() {
+                int n = 0;
+                if (lane == 0) n = atomicAdd(&p.header->taken, 1);
+                it = static_cast<int>(gridDim.x) + __shfl_sync(0xffffffffu, n, 0);
+                load_record(it);
+            };
+            if (x.T == 0) take_next();
             for (int i = 0; i < 2 && ok; ++i) {
                 if (x.e[i] == x.a[i]) continue;
                 if (kq[i] > 0 && !ptx::mbar_wait_warp(&bar->q_empty[i], (kq[i] - 1) & 1, abort_flag)) { ok = false; break; }
@@ -685,6 +699,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 page = look_up(x, u + 1);  // one tile ahead
                 load_tile(x, &tm_k, sK + sk * C::TILE_BYTES, &bar->k_full[sk], x.J0 + x.tile(u), now,
                           p.debug_drop_copy && issued == 0 && blockIdx.x == 0);
+                if (u == take) take_next();
                 ++issued;
                 if (++sk == NK) {
                     sk = 0;
@@ -709,10 +724,11 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
         int sv = 0, issued = 0;
         uint32_t free_par = 1;
         bool ok = true;
-        for (int rnd = 0, it = blockIdx.x; ok && it < n_items; it = item_of_round(++rnd, blockIdx.x, gridDim.x)) {
+        for (int rnd = 0; ok; ++rnd) {
             const int ws = rnd % kWorkRing;
             if (!ptx::mbar_wait_warp(&bar->work_full[ws], (rnd / kWorkRing) & 1, abort_flag)) { ok = false; break; }
             const PackedWork x = bar->work[ws];
+            if (x.T < 0) break;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bar->work_empty[ws]);
             int page = look_up(x, 0);
@@ -808,11 +824,12 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
             issued_any = true;
             return true;
         };
-        for (int rnd = 0, it = blockIdx.x; ok && it < n_items; it = item_of_round(++rnd, blockIdx.x, gridDim.x)) {
+        for (int rnd = 0; ok; ++rnd) {
             const int ws = rnd % kWorkRing;
             if (!ptx::mbar_wait_warp(&bar->work_full[ws], (rnd / kWorkRing) & 1, abort_flag)) { ok = false; break; }
             const PackedWork& x = bar->work[ws];
             const int T = x.T, key0 = x.J0 * C::BN, half = x.half;
+            if (T < 0) break;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 a[i] = x.a[i];
@@ -887,10 +904,11 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
         uint32_t par = 0;
         auto parity = [&](uint32_t bit) { return (par & bit) ? 1u : 0u; };
         int g = 0;  // key tiles of the items before
-        for (int rnd = 0, it = blockIdx.x; ok && it < n_items; it = item_of_round(++rnd, blockIdx.x, gridDim.x)) {
+        for (int rnd = 0; ok; ++rnd) {
             const int ws = rnd % kWorkRing;
             if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->work_full[ws], (rnd / kWorkRing) & 1, abort_flag))) { ok = false; break; }
             const PackedWork& x = bar->work[ws];  // kept until the item is done: registers are scarce here
+            if (x.T < 0) break;
             auto release_work = [&]() {
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&bar->work_empty[ws]);

@@ -7,8 +7,8 @@
 //             tiles; TT = 128 / G tokens times the G query heads of a K/V head fill a tile) against a
 //             range of 128-key tiles. Each item stands for every K/V head.
 //   backward  an item is one 128-key tile of one sequence.
-// Items are listed longest first (a counting sort by their key or query tiles), so that CTAs that
-// take them in rounds finish together. Where the longest blocks would leave most CTAs idle at the end,
+// Items are listed longest first (a counting sort by what they cost), and a CTA that is done with one
+// takes the next, so that all finish together. Where the longest blocks would leave most CTAs idle at the end,
 // long forward blocks are cut into parts along the keys; the warp that finishes a block's last part
 // joins the parts' softmax states in ascending order, so the result depends on the lengths alone, not
 // on timing.
@@ -65,7 +65,7 @@ struct PlanHeader {
     int n_items;   // forward items (each for every K/V head); backward tiles
     int n_slots;   // partial-state slots in use
     int bad;       // the offsets are invalid: there are no items
-    int pad;
+    int taken;     // items taken beyond the first of every CTA
 };
 
 // Key tiles visible to tokens [first, last] (positions) of a sequence of kv_len keys: [jb, jb + n).
@@ -89,14 +89,19 @@ ATTN_HD void query_tiles(int t, int n, int causal, int window, int& ib, int& ie)
     if (window > 0 && window < n) ie = plan_min(ie, (t * 128 + 127 + window - 1) / 128 + 1);
 }
 
-// Longest part the split rule leaves: the whole call's key tiles (every K/V head) over kPlanWaves
+// What `tiles` key tiles cost, in steps of a CTA (one key tile for both query tiles): a block of one
+// query tile (at most TT tokens) has both halves of its keys worked on at once, so a step takes two of
+// its tiles; 5/8 and not 1/2, because it also reads two tiles a step.
+ATTN_HD int plan_cost(int tiles, int one_tile) { return one_tile ? (5 * tiles + 7) / 8 : tiles; }
+
+// Longest part the split rule leaves: the whole call's cost (every K/V head) over kPlanWaves
 // parts per CTA, at least kPlanMinTiles.
-ATTN_HD int plan_limit(long long tiles_per_head, int Hkv) {
-    const long long share = (tiles_per_head * Hkv + kPlanWaves * kPlanSms - 1) / (kPlanWaves * kPlanSms);
+ATTN_HD int plan_limit(long long cost_per_head, int Hkv) {
+    const long long share = (cost_per_head * Hkv + kPlanWaves * kPlanSms - 1) / (kPlanWaves * kPlanSms);
     return share < kPlanMinTiles ? kPlanMinTiles : share > 0x3fffffff ? 0x3fffffff : static_cast<int>(share);
 }
-ATTN_HD int plan_parts(int tiles, int limit) {
-    const int p = tiles > limit ? plan_ceil(tiles, limit) : 1;
+ATTN_HD int plan_parts(int cost, int limit) {
+    const int p = cost > limit ? plan_ceil(cost, limit) : 1;
     return p > kPlanMaxParts ? kPlanMaxParts : p;
 }
 // Part i of `parts` over `tiles` tiles: [begin, end), sizes differing by at most one.
@@ -106,10 +111,11 @@ ATTN_HD void plan_part(int tiles, int parts, int i, int& begin, int& end) {
     end = begin + q + (i < r ? 1 : 0);
 }
 
-// Partial-state slots a plan can need (each for every K/V head): a block is cut only when it has
-// more than `limit` tiles, and then into fewer than 2 tiles / limit parts; summed over the blocks
+// Partial-state slots a plan can need (each for every K/V head): a block is cut only when it costs
+// more than `limit`, and then into fewer than 2 cost / limit parts; summed over the blocks
 // that is less than 2 kPlanWaves kPlanSms / Hkv. Nor can `blocks` blocks of at most max_tiles tiles
 // be cut into more than blocks * ceil(max_tiles / kPlanMinTiles) parts.
+// (No block costs more than its tiles.)
 ATTN_HD long long plan_slots(long long blocks, long long max_tiles, int Hkv) {
     if (max_tiles <= kPlanMinTiles) return 0;
     const long long a = 2LL * kPlanWaves * kPlanSms / Hkv + 1;
