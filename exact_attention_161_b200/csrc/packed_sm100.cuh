@@ -415,6 +415,7 @@ constexpr int kWorkRing = 4;
 template <int NK, int NV>
 struct PackedBarriers : FwdBarriers<NK, NV> {
     uint64_t work_full[kWorkRing], work_empty[kWorkRing];
+    uint64_t p_half[2];
     uint64_t s_free[2], pv_done[2], drain_outputs;  // kSplitP
     uint64_t side_full, side_empty;  // the second side's statistics
     PackedWork work[kWorkRing];
@@ -568,6 +569,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
             ptx::mbar_init(&bar->p_full[i], 128);
             ptx::mbar_init(&bar->o_final[i], 1);
             ptx::mbar_init(&bar->o_empty[i], 128);
+            ptx::mbar_init(&bar->p_half[i], 128);
             ptx::mbar_init(&bar->s_free[i], 128);
             ptx::mbar_init(&bar->pv_done[i], 1);
         }
@@ -801,22 +803,28 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 if (!ptx::mbar_wait_warp(&bar->o_empty[i], o_par[i], abort_flag)) return false;
                 o_par[i] ^= 1;
             }
-            if (!ptx::mbar_wait_warp(&bar->p_full[i], p_par[i], abort_flag)) return false;
-            p_par[i] ^= 1;
+            if (!ptx::mbar_wait_warp(&bar->p_half[i], p_par[i], abort_flag)) return false;
             ptx::tc_fence_after();
             const uint32_t d_o = tm + C::tmem_o(i), d_p = tm + tmem_p(i);
             const uint64_t vb = v_d + sv * TILE16;
             const uint32_t acc = first ? 0u : 1u;
-            if (keys > 112) {
+            auto slices = [&](int k0) {
+                if (keys > 112) {
 #pragma unroll
-                for (int kk = 0; kk < C::O_KSTEPS; ++kk)
-                    ptx::mma_ts_if(issue, d_o, d_p + kk * 8, vb + kk * ((C::O_ROWS * 128) >> 4), IDESC_O, kk > 0 ? 1u : acc);
-            } else {
+                    for (int kk = k0; kk < k0 + C::O_KSTEPS / 2; ++kk)
+                        ptx::mma_ts_if(issue, d_o, d_p + kk * 8, vb + kk * ((C::O_ROWS * 128) >> 4), IDESC_O, kk > 0 ? 1u : acc);
+                } else {
 #pragma unroll
-                for (int kk = 0; kk < C::O_KSTEPS - 1; ++kk)
-                    ptx::mma_ts_if(kk * 16 < keys ? issue : 0u, d_o, d_p + kk * 8, vb + kk * ((C::O_ROWS * 128) >> 4), IDESC_O,
-                                   kk > 0 ? 1u : acc);
-            }
+                    for (int kk = k0; kk < k0 + C::O_KSTEPS / 2; ++kk)
+                        ptx::mma_ts_if(kk * 16 < keys ? issue : 0u, d_o, d_p + kk * 8, vb + kk * ((C::O_ROWS * 128) >> 4),
+                                       IDESC_O, kk > 0 ? 1u : acc);
+                }
+            };
+            slices(0);
+            if (!ptx::mbar_wait_warp(&bar->p_full[i], p_par[i], abort_flag)) return false;
+            p_par[i] ^= 1;
+            ptx::tc_fence_after();
+            slices(C::O_KSTEPS / 2);
             if (kSplitP)
                 ptx::mma_commit_if(issue, &bar->pv_done[i]);
             else if (last)
@@ -963,39 +971,11 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 }
                 const float m_eff = (m_used == -INFINITY) ? 0.f : m_used;
                 const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(-m_eff, -m_eff);
-                float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0, acc2 = acc0, acc3 = acc0;
-                uint32_t pk[C::P_COLS];
-#pragma unroll
-                for (int k = 0; k < C::BN; k += 8) {
-                    float2 x0 = ptx::ffma2(make_float2(s[k], s[k + 1]), sl2, nm2);
-                    float2 x1 = ptx::ffma2(make_float2(s[k + 2], s[k + 3]), sl2, nm2);
-                    float2 x2 = ptx::ffma2(make_float2(s[k + 4], s[k + 5]), sl2, nm2);
-                    float2 x3 = ptx::ffma2(make_float2(s[k + 6], s[k + 7]), sl2, nm2);
-                    x0 = make_float2(ptx::ex2(x0.x), ptx::ex2(x0.y));
-                    x1 = make_float2(ptx::ex2(x1.x), ptx::ex2(x1.y));
-                    x2 = make_float2(ptx::ex2(x2.x), ptx::ex2(x2.y));
-                    // 1/8 of the exponentials on the FMA pipe, as in attn_fwd_kernel
-                    if ((k / 8) % 2 == 0)
-                        x3 = make_float2(ptx::ex2_poly4(x3.x), ptx::ex2_poly4(x3.y));
-                    else
-                        x3 = make_float2(ptx::ex2(x3.x), ptx::ex2(x3.y));
-                    acc0 = ptx::fadd2(acc0, x0);
-                    acc1 = ptx::fadd2(acc1, x1);
-                    acc2 = ptx::fadd2(acc2, x2);
-                    acc3 = ptx::fadd2(acc3, x3);
-                    pk[k / 2] = ptx::pack_bf16x2(x0.x, x0.y);
-                    pk[k / 2 + 1] = ptx::pack_bf16x2(x1.x, x1.y);
-                    pk[k / 2 + 2] = ptx::pack_bf16x2(x2.x, x2.y);
-                    pk[k / 2 + 3] = ptx::pack_bf16x2(x3.x, x3.y);
-                }
-                const float2 sum = ptx::fadd2(ptx::fadd2(acc0, acc1), ptx::fadd2(acc2, acc3));
-                l = l * alpha + (sum.x + sum.y);
                 if constexpr (kSplitP) {
                     // P and O are free once the product before has completed
                     if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->pv_done[wg], parity(kTiles) ^ 1, abort_flag))) { ok = false; break; }
                     ptx::tc_fence_after();
                 }
-                ptx::tmem_st64(t_p, pk);
                 // the end of the sequence inside a 16-key slice: zero the slice's other V rows (both
                 // query tiles may do it: the same zeros, before either P is handed over)
                 const int tail = x.kv_len - j0;
@@ -1010,22 +990,55 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 }
                 if (c > 0 && __any_sync(0xffffffffu, rescale)) {
                     const float2 al2 = make_float2(alpha, alpha);
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 16; ++cc) {
+                        uint32_t v[16];
+                        ptx::tmem_ld16(t_o + cc * 16, v);
 #pragma unroll
-                    for (int cc = 0; cc < D / 32; ++cc) {
-                        uint32_t v[32];
-                        ptx::tmem_ld32(t_o + cc * 32, v);
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
+                        for (int k = 0; k < 16; k += 2) {
                             const float2 y =
                                 ptx::fmul2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), al2);
                             v[k] = __float_as_uint(y.x);
                             v[k + 1] = __float_as_uint(y.y);
                         }
-                        ptx::tmem_st32(t_o + cc * 32, v);
+                        ptx::tmem_st16(t_o + cc * 16, v);
                     }
                 }
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(&bar->p_full[wg]);
+                // P in two halves: the product starts on the first while the second is computed
+                float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0, acc2 = acc0, acc3 = acc0;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[C::P_COLS / 2];
+#pragma unroll
+                    for (int k = 0; k < C::BN / 2; k += 8) {
+                        const float* z = s + half * (C::BN / 2) + k;
+                        float2 x0 = ptx::ffma2(make_float2(z[0], z[1]), sl2, nm2);
+                        float2 x1 = ptx::ffma2(make_float2(z[2], z[3]), sl2, nm2);
+                        float2 x2 = ptx::ffma2(make_float2(z[4], z[5]), sl2, nm2);
+                        float2 x3 = ptx::ffma2(make_float2(z[6], z[7]), sl2, nm2);
+                        x0 = make_float2(ptx::ex2(x0.x), ptx::ex2(x0.y));
+                        x1 = make_float2(ptx::ex2(x1.x), ptx::ex2(x1.y));
+                        x2 = make_float2(ptx::ex2(x2.x), ptx::ex2(x2.y));
+                        // 1/8 of the exponentials on the FMA pipe, as in attn_fwd_kernel
+                        if ((k / 8) % 2 == 0)
+                            x3 = make_float2(ptx::ex2_poly4(x3.x), ptx::ex2_poly4(x3.y));
+                        else
+                            x3 = make_float2(ptx::ex2(x3.x), ptx::ex2(x3.y));
+                        acc0 = ptx::fadd2(acc0, x0);
+                        acc1 = ptx::fadd2(acc1, x1);
+                        acc2 = ptx::fadd2(acc2, x2);
+                        acc3 = ptx::fadd2(acc3, x3);
+                        pk[k / 2] = ptx::pack_bf16x2(x0.x, x0.y);
+                        pk[k / 2 + 1] = ptx::pack_bf16x2(x1.x, x1.y);
+                        pk[k / 2 + 2] = ptx::pack_bf16x2(x2.x, x2.y);
+                        pk[k / 2 + 3] = ptx::pack_bf16x2(x3.x, x3.y);
+                    }
+                    ptx::tmem_st32(t_p + half * (C::P_COLS / 2), pk);
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(half ? &bar->p_full[wg] : &bar->p_half[wg]);
+                }
+                const float2 sum = ptx::fadd2(ptx::fadd2(acc0, acc1), ptx::fadd2(acc2, acc3));
+                l = l * alpha + (sum.x + sum.y);
                 par ^= kTiles;
             }
             if (!ok) break;
