@@ -1152,7 +1152,7 @@ attn_status attn_packed_fwd(const void* q, const void* k, const void* v, int64_t
     c.Hq = Hq;
     c.Hkv = Hkv;
     c.causal = causal;
-    c.window = window > 0 ? window : 0;
+    c.window = window > 0 && window < T ? window : 0;  // (at T or more it cuts nothing, and sums with it stay ints)
     c.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D));
     c.o = o;
     c.lse = lse;
@@ -1194,7 +1194,7 @@ attn_status attn_packed_bwd(const void* q, const void* k, const void* v, int64_t
     int dev = 0;
     CUDA_TRY(cudaGetDevice(&dev));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    window = window > 0 ? window : 0;
+    window = window > 0 && window < T ? window : 0;
     return D == 64 ? launch_packed_bwd<64>(q, k, v, q_stride, k_stride, v_stride, o, lse, dout, dq, dk, dv, dq_stride,
                                            dk_stride, dv_stride, cu_seqlens, num_seqs, T, Hq, Hkv, causal, window, scale,
                                            workspace, s, dev)
@@ -1264,7 +1264,7 @@ attn_status attn_chunk_paged(const void* q, const void* k_new, const void* v_new
     c.Hq = Hq;
     c.Hkv = Hkv;
     c.causal = 1;
-    c.window = window > 0 ? window : 0;
+    c.window = window > 0 && window < max_blocks_per_seq * page_size ? window : 0;
     c.max_blocks = max_blocks_per_seq;
     c.num_pages = num_pages;
     c.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D));

@@ -598,7 +598,6 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             int hi = p.window > 0 ? key + p.window - 1 - c0 : 32;
             bool past_end = false;  // packed: a query column or the key row lies behind the sequence
             if constexpr (kPacked) {
-                if (p.window > 0) hi = p.window >= N ? 32 : hi;  // (key + window stays an int)
                 past_end = key >= N || c0 + 32 > N;
                 if (past_end) hi = key >= N ? -1 : min(hi, N - 1 - c0);
             }
