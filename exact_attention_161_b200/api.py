@@ -371,12 +371,12 @@ def attn_packed_fwd(q, k, v, cu_seqlens, causal=False, window=0, scale=0.0, o=No
         raise ValueError("o must be [T, Hq, D] and lse [Hq, T]")
 
     def call(st):
-        out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device) if o is None else o
-        stats = torch.empty((Hq, T), dtype=_F32, device=q.device) if lse is None and want_lse else lse
+        out = q.new_empty((T, Hq, D)) if o is None else o
+        stats = q.new_empty((Hq, T), dtype=_F32) if lse is None and want_lse else lse
         (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", dev), _rows(k, "k", dev), _rows(v, "v", dev)
         ws = workspace
         if ws is None:
-            ws = torch.empty(lib.attn_packed_fwd_workspace_size(T, S, Hq, Hkv, D), dtype=_U8, device=q.device)
+            ws = q.new_empty(lib.attn_packed_fwd_workspace_size(T, S, Hq, Hkv, D), dtype=_U8)
         _check(lib.attn_packed_fwd(qp, kp, vp, qs, ks, vs, _ptr(cu_seqlens, "cu_seqlens", _I32, dev), S, T, Hq, Hkv, D,
                                    bool(causal), window, scale, _ptr(out, "o", _BF16, dev),
                                    None if stats is None else _ptr(stats, "lse", _F32, dev),
@@ -405,13 +405,13 @@ def attn_packed_bwd(q, k, v, o, lse, dout, cu_seqlens, causal=False, window=0, s
             raise ValueError("%s has another shape than its input" % name)
 
     def call(st):
-        gq, gk, gv = (torch.empty(like.shape, dtype=_BF16, device=q.device) if t is None else t
+        gq, gk, gv = (q.new_empty(like.shape) if t is None else t
                       for t, like in ((dq, q), (dk, k), (dv, v)))
         (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", dev), _rows(k, "k", dev), _rows(v, "v", dev)
         (gqp, gqs), (gkp, gks), (gvp, gvs) = _rows(gq, "dq", dev), _rows(gk, "dk", dev), _rows(gv, "dv", dev)
         ws = workspace
         if ws is None:
-            ws = torch.empty(lib.attn_packed_bwd_workspace_size(T, S, Hq, D), dtype=_U8, device=q.device)
+            ws = q.new_empty(lib.attn_packed_bwd_workspace_size(T, S, Hq, D), dtype=_U8)
         _check(lib.attn_packed_bwd(qp, kp, vp, qs, ks, vs, _ptr(o, "o", _BF16, dev), _ptr(lse, "lse", _F32, dev),
                                    _ptr(dout, "dout", _BF16, dev), gqp, gkp, gvp, gqs, gks, gvs,
                                    _ptr(cu_seqlens, "cu_seqlens", _I32, dev), S, T, Hq, Hkv, D, bool(causal), window,
@@ -449,8 +449,8 @@ def attn_chunk_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, k_n
     max_blocks, dev = block_table.shape[1], _device_of(q)
 
     def call(st):
-        out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device) if o is None else o
-        stats = torch.empty((T, Hq), dtype=_F32, device=q.device) if lse is None and want_lse else lse
+        out = q.new_empty((T, Hq, D)) if o is None else o
+        stats = q.new_empty((T, Hq), dtype=_F32) if lse is None and want_lse else lse
         qp, qs = _rows(q, "q", dev)
         kp, ks, vp, vs = None, 0, None, 0
         if k_new is not None:
@@ -458,7 +458,7 @@ def attn_chunk_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, k_n
         ws = workspace
         if ws is None:
             need = lib.attn_chunk_workspace_size(T, S, max_blocks, page_size, Hq, Hkv, D)
-            ws = torch.empty(need, dtype=_U8, device=q.device)
+            ws = q.new_empty(need, dtype=_U8)
         _check(lib.attn_chunk_paged(qp, kp, vp, qs, ks, vs, _ptr(k_pages, "k_pages", _BF16, dev),
                                     _ptr(v_pages, "v_pages", _BF16, dev), _ptr(block_table, "block_table", _I32, dev),
                                     _ptr(seq_lens, "seq_lens", _I32, dev), _ptr(cu_seqlens, "cu_seqlens", _I32, dev), S,
@@ -488,8 +488,8 @@ def attn_rope_axes(q, k, positions, sections, interleave_axes=False, per_axis_fr
     dev = _device_of(q)
 
     def call(st):
-        yq = torch.empty((T, Hq, D), dtype=_BF16, device=q.device) if q_out is None else q_out
-        yk = torch.empty(k.shape, dtype=_BF16, device=q.device) if k_out is None and k is not None else k_out
+        yq = q.new_empty((T, Hq, D)) if q_out is None else q_out
+        yk = q.new_empty(k.shape) if k_out is None and k is not None else k_out
         (qp, qs), (yqp, yqs) = _rows(q, "q", dev), _rows(yq, "q_out", dev)
         Hk, kp, ks, ykp, yks = 0, None, 0, None, 0
         if k is not None:

@@ -656,7 +656,7 @@ attn_status launch_packed(const PackedCall& c, cudaStream_t stream, int dev) {
         ap.vs = c.vs;
         ap.max_blocks = c.max_blocks;
         ap.num_pages = c.num_pages;
-        const long long want = (static_cast<long long>(c.T) * c.Hkv + 31) / 32;
+        const long long want = (static_cast<long long>(c.T) + 31) / 32;  // a warp per token
         append_blocks = static_cast<unsigned>(want < 2LL * sms ? want : 2LL * sms);
     }
     attn::packed_plan_kernel<D, kPaged, false><<<1 + append_blocks, attn::kPlanThreads, 0, stream>>>(pl, ap);

@@ -292,8 +292,8 @@ struct AppendParams {
     int max_blocks, num_pages;
 };
 
-// Block 0 builds the plan; with kPaged the other blocks append the new tokens meanwhile, a warp per
-// (token, K/V head): 2 D elements each way.
+// Block 0 builds the plan; with kPaged the other blocks append the new tokens meanwhile, a warp per token:
+// 2 D elements each way for every K/V head.
 template <int D, bool kPaged, bool kBwd>
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PlanParams p, const AppendParams a) {
     ptx::grid_launch_dependents();  // the attention kernel's set-up may overlap; it waits for this grid
@@ -303,20 +303,19 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PlanPar
     }
     if constexpr (kPaged) {
         const int lane = threadIdx.x & 31;
-        const long long warps = static_cast<long long>(gridDim.x - 1) * (kPlanThreads / 32);
-        const long long rows = static_cast<long long>(p.T) * p.Hkv;
-        constexpr int LPR = D / 8;  // lanes per row of 16-byte pieces
-        for (long long w = static_cast<long long>(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5); w < rows;
-             w += warps) {
-            const int t = static_cast<int>(w / p.Hkv), g = static_cast<int>(w % p.Hkv);
-            // the sequence of token t: the last s with cu[s] <= t (invalid offsets end anywhere in [0, S))
-            int lo = 0, hi = p.S - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (p.cu[mid] <= t)
-                    lo = mid;
-                else
-                    hi = mid - 1;
+        const int warps = static_cast<int>(gridDim.x - 1) * (kPlanThreads / 32);
+        constexpr int LPR = D / 8;       // lanes per row of 16-byte pieces
+        constexpr int HPW = 32 / (2 * LPR);  // heads a warp takes at a time (K and V rows)
+        for (int t = static_cast<int>(blockIdx.x - 1) * (kPlanThreads / 32) + (threadIdx.x >> 5); t < p.T; t += warps) {
+            // the sequence of token t: the last s with cu[s] <= t, 32 candidates a round (invalid offsets
+            // end anywhere in [0, S))
+            int lo = 0, n = p.S;
+            while (n > 1) {
+                const int step = plan_ceil(n, 32);
+                const unsigned below = __ballot_sync(0xffffffffu, lane * step < n && p.cu[lo + min(lane * step, n - 1)] <= t);
+                const int c = max(1, __popc(below)) - 1;
+                lo += c * step;
+                n = min(step, n - c * step);
             }
             const int c0 = p.cu[lo], c1 = p.cu[lo + 1], len = p.seq_lens[lo];
             if (t < c0 || t >= c1 || c0 < 0 || c1 > p.T) continue;       // behind the last sequence
@@ -327,14 +326,16 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PlanPar
                 if (lane == 0) raise_status(kStatusBadPage);
                 continue;
             }
-            const size_t dst = ((static_cast<size_t>(page) * p.Hkv + g) * kPageSize + pos % kPageSize) * D;
-            if (lane < 2 * LPR) {
-                const bool is_v = lane >= LPR;
-                const int c = is_v ? lane - LPR : lane;
-                const __nv_bfloat16* src = (is_v ? a.v_new + t * a.vs : a.k_new + t * a.ks) + static_cast<size_t>(g) * D;
-                __nv_bfloat16* out = (is_v ? a.v_pages : a.k_pages) + dst;
-                reinterpret_cast<uint4*>(out)[c] = __ldg(reinterpret_cast<const uint4*>(src) + c);
-            }
+            const int sub = lane / (2 * LPR), l = lane % (2 * LPR);
+            const bool is_v = l >= LPR;
+            const int c = is_v ? l - LPR : l;
+            const __nv_bfloat16* src = is_v ? a.v_new + t * a.vs : a.k_new + t * a.ks;
+            __nv_bfloat16* out = (is_v ? a.v_pages : a.k_pages) +
+                                 (static_cast<size_t>(page) * p.Hkv * kPageSize + pos % kPageSize) * D;
+#pragma unroll 4
+            for (int g = sub; g < p.Hkv; g += HPW)
+                reinterpret_cast<uint4*>(out + static_cast<size_t>(g) * kPageSize * D)[c] =
+                    __ldg(reinterpret_cast<const uint4*>(src + static_cast<size_t>(g) * D) + c);
         }
     }
 }
