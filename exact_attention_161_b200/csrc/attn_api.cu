@@ -717,6 +717,7 @@ attn_status launch_packed_bwd(const void* q, const void* k, const void* v, long 
     pl.prefix = reinterpret_cast<int*>(w + L.prefix);
     pl.tiles = reinterpret_cast<attn::PackedTile*>(w + L.tiles);
     pl.order = reinterpret_cast<int*>(w + L.order);
+    pl.start = reinterpret_cast<int*>(w + L.start);
     pl.S = S;
     pl.T = T;
     pl.TT = 64;

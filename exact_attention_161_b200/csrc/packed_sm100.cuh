@@ -44,7 +44,8 @@ struct PlanParams {
     PackedItem* items;
     int* count;               // finished parts of [slot of part 0][K/V head][softmax warp]
     PackedTile* tiles;        // backward: natural order
-    int* order;               // backward: tile numbers, most query tiles first
+    int* order;               // backward: tile numbers, longest sequence first
+    int* start;               // backward: [S] where each sequence's tiles stand in the order
     int S, T, TT, Hkv, causal, window;
     int max_len;              // paged: tokens a block-table row can hold
 };
@@ -135,10 +136,7 @@ __device__ void build_plan(const PlanParams& p) {
     }
     __syncthreads();
 
-    struct Block {
-        int s, first, n, tiles, cost, kv_len;  // sequence, first token and tokens of the block, its tiles, keys
-    };
-    auto block_of = [&](int b) {
+    auto seq_of = [&](int b) {
         int lo = 0, hi = p.S - 1;  // the last sequence whose first block is <= b (empty ones never are the last)
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -147,27 +145,71 @@ __device__ void build_plan(const PlanParams& p) {
             else
                 hi = mid - 1;
         }
+        return lo;
+    };
+    if constexpr (kBwd) {
+        // sequences sorted by length (a counting sort by their tiles); a sequence's tiles in their own order,
+        // which with a causal mask is most query tiles first
+        s_hist[tid] = 0;
+        __syncthreads();
+        int most = 1;
+        for (int s = tid; s < p.S; s += kPlanThreads) most = max(most, pre[s + 1] - pre[s]);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if ((tid & 31) == 0) atomicMax(&s_max, most);
+        __syncthreads();
+        auto bucket = [&](int tiles) {
+            return kPlanBuckets - 1 - static_cast<int>(static_cast<long long>(tiles) * (kPlanBuckets - 1) / s_max);
+        };
+        for (int s = tid; s < p.S; s += kPlanThreads) {
+            const int tiles = pre[s + 1] - pre[s];
+            if (tiles > 0) atomicAdd(&s_hist[bucket(tiles)], tiles);
+        }
+        __syncthreads();
+        int total;
+        const int first = plan_scan(s_hist[tid], s_warp, total);
+        s_hist[tid] = first;
+        __syncthreads();
+        for (int s = tid; s < p.S; s += kPlanThreads) {
+            const int tiles = pre[s + 1] - pre[s];
+            if (tiles > 0) p.start[s] = atomicAdd(&s_hist[bucket(tiles)], tiles);
+        }
+        __syncthreads();
+        for (int b = tid; b < n_blocks; b += kPlanThreads) {
+            const int s = seq_of(b);
+            PackedTile t;
+            t.row0 = p.cu[s];
+            t.n = p.cu[s + 1] - t.row0;
+            t.base = pre[s];
+            t.t = b - t.base;
+            p.tiles[b] = t;
+            p.order[p.start[s] + t.t] = b;
+        }
+        if (tid == 0) {
+            PlanHeader h{n_blocks, 0, 0, 0};
+            *p.header = h;
+        }
+        return;
+    }
+
+    struct Block {
+        int s, first, n, tiles, cost, kv_len;  // sequence, first token and tokens of the block, its tiles, keys
+    };
+    auto block_of = [&](int b) {
+        const int lo = seq_of(b);
         Block x;
         x.s = lo;
         const int n = p.cu[lo + 1] - p.cu[lo];
         x.first = (b - pre[lo]) * tok;
         x.n = min(tok, n - x.first);
-        if constexpr (kBwd) {
-            int ib, ie;
-            query_tiles(b - pre[lo], n, p.causal, p.window, ib, ie);
-            x.tiles = x.cost = max(0, ie - ib);
-            x.kv_len = n;
-        } else {
-            int len = n;
-            if (p.seq_lens != nullptr) {
-                len = p.seq_lens[lo];
-                if (len < n || len > p.max_len) len = -1;
-            }
-            x.kv_len = len;
-            const int pos = len - n + x.first;
-            x.tiles = len < 0 ? 0 : key_tiles(pos, pos + x.n - 1, len, p.causal, p.window).n;
-            x.cost = plan_cost(x.tiles, x.n <= p.TT);
+        int len = n;
+        if (p.seq_lens != nullptr) {
+            len = p.seq_lens[lo];
+            if (len < n || len > p.max_len) len = -1;
         }
+        x.kv_len = len;
+        const int pos = len - n + x.first;
+        x.tiles = len < 0 ? 0 : key_tiles(pos, pos + x.n - 1, len, p.causal, p.window).n;
+        x.cost = plan_cost(x.tiles, x.n <= p.TT);
         return x;
     };
     Block mine{};  // this thread's first block is kept; further ones are looked up again in each walk
@@ -189,10 +231,10 @@ __device__ void build_plan(const PlanParams& p) {
         atomicMax(&s_max, most);
     }
     __syncthreads();
-    const int limit = kBwd ? 0x3fffffff : plan_limit(static_cast<long long>(s_sum), p.Hkv);
+    const int limit = plan_limit(static_cast<long long>(s_sum), p.Hkv);
     const int longest = s_max;
     auto bucket = [&](const Block& x, int tiles) {  // of an item of block x
-        const long long cost = kBwd ? tiles : plan_cost(tiles, x.n <= p.TT);
+        const long long cost = plan_cost(tiles, x.n <= p.TT);
         return kPlanBuckets - 1 - static_cast<int>(cost * (kPlanBuckets - 1) / longest);
     };
     int n_items = 0;
@@ -211,7 +253,7 @@ __device__ void build_plan(const PlanParams& p) {
         const int mine_n = s_hist[tid];
         const int start = plan_scan(mine_n, s_warp, n_items);
         s_hist[tid] = start;
-        if (!kBwd && longest > limit && mine_n > 0) {
+        if (longest > limit && mine_n > 0) {
             // G-th items of this length
             const int first = plan_ceil_div(static_cast<long long>(start) * p.Hkv, kPlanSms);
             const int last = plan_ceil_div(static_cast<long long>(start + mine_n) * p.Hkv, kPlanSms);
@@ -220,7 +262,7 @@ __device__ void build_plan(const PlanParams& p) {
         }
         __syncthreads();
     };
-    if (!kBwd && longest > limit) {
+    if (longest > limit) {
         sort_items(true);
         cut = true;
         const int with = s_load[1] + kPlanJoinTiles;
@@ -239,38 +281,28 @@ __device__ void build_plan(const PlanParams& p) {
 
     for (int b = tid; b < n_blocks; b += kPlanThreads) {
         const Block x = get(b);
-        if constexpr (kBwd) {
-            PackedTile t;
-            t.row0 = p.cu[x.s];
-            t.n = x.kv_len;
-            t.base = pre[x.s];
-            t.t = b - t.base;
-            p.tiles[b] = t;
-            p.order[atomicAdd(&s_hist[bucket(x, x.tiles)], 1)] = b;
-        } else {
-            const int parts = cut ? plan_parts(x.cost, limit) : 1;
-            const int row0 = p.cu[x.s];
-            const int n = p.cu[x.s + 1] - row0;
-            PackedItem it;
-            it.q_row = row0 + x.first;
-            it.pos0 = x.kv_len < 0 ? 0 : x.kv_len - n + x.first;
-            it.kv = p.seq_lens != nullptr ? x.s : row0;
-            it.kv_len = x.kv_len;
-            it.slot = 0;
-            if (parts > 1) {
-                it.slot = atomicAdd(&s_slots, parts);
-                for (int i = 0; i < p.Hkv * kPlanWarps; ++i) p.count[static_cast<size_t>(it.slot) * p.Hkv * kPlanWarps + i] = 0;
-            }
-            const int jb =
-                x.kv_len < 0 ? 0 : key_tiles(it.pos0, it.pos0 + x.n - 1, x.kv_len, p.causal, p.window).jb;
-            for (int i = 0; i < parts; ++i) {
-                int b0, b1;
-                plan_part(x.tiles, parts, i, b0, b1);
-                it.jb = jb + b0;
-                it.n_tiles = b1 - b0;
-                it.meta = make_meta(x.n, i, parts);
-                p.items[atomicAdd(&s_hist[bucket(x, it.n_tiles)], 1)] = it;
-            }
+        const int parts = cut ? plan_parts(x.cost, limit) : 1;
+        const int row0 = p.cu[x.s];
+        const int n = p.cu[x.s + 1] - row0;
+        PackedItem it;
+        it.q_row = row0 + x.first;
+        it.pos0 = x.kv_len < 0 ? 0 : x.kv_len - n + x.first;
+        it.kv = p.seq_lens != nullptr ? x.s : row0;
+        it.kv_len = x.kv_len;
+        it.slot = 0;
+        if (parts > 1) {
+            it.slot = atomicAdd(&s_slots, parts);
+            for (int i = 0; i < p.Hkv * kPlanWarps; ++i) p.count[static_cast<size_t>(it.slot) * p.Hkv * kPlanWarps + i] = 0;
+        }
+        const int jb =
+            x.kv_len < 0 ? 0 : key_tiles(it.pos0, it.pos0 + x.n - 1, x.kv_len, p.causal, p.window).jb;
+        for (int i = 0; i < parts; ++i) {
+            int b0, b1;
+            plan_part(x.tiles, parts, i, b0, b1);
+            it.jb = jb + b0;
+            it.n_tiles = b1 - b0;
+            it.meta = make_meta(x.n, i, parts);
+            p.items[atomicAdd(&s_hist[bucket(x, it.n_tiles)], 1)] = it;
         }
     }
     __syncthreads();

@@ -7,8 +7,9 @@
 //             tiles; TT = 128 / G tokens times the G query heads of a K/V head fill a tile) against a
 //             range of 128-key tiles. Each item stands for every K/V head.
 //   backward  an item is one 128-key tile of one sequence.
-// Items are listed longest first (a counting sort by what they cost), and a CTA that is done with one
-// takes the next, so that all finish together. Where the longest blocks would leave most CTAs idle at the end,
+// Forward items are listed longest first (a counting sort by what they cost), and a CTA that is done with
+// one takes the next, so that all finish together. Backward tiles are listed sequence by sequence, the
+// longest first, so that the sequences' queries and dq sums stay in L2 while their tiles are worked on. Where the longest blocks would leave most CTAs idle at the end,
 // long forward blocks are cut into parts along the keys; the warp that finishes a block's last part
 // joins the parts' softmax states in ascending order, so the result depends on the lengths alone, not
 // on timing.
@@ -150,7 +151,7 @@ ATTN_HD PlanLayout plan_layout(long long T, long long S, int TT, long long max_k
 
 // Byte offsets of a backward plan and its arrays: tiles <= T / 128 + S, each of 128 padded rows.
 struct BwdPlanLayout {
-    size_t header, prefix, tiles, order, vec, dqacc, total;
+    size_t header, prefix, start, tiles, order, vec, dqacc, total;
     long long max_tiles;
 };
 ATTN_HD BwdPlanLayout bwd_plan_layout(long long T, long long S, int Hq, int D) {
@@ -158,7 +159,8 @@ ATTN_HD BwdPlanLayout bwd_plan_layout(long long T, long long S, int Hq, int D) {
     L.max_tiles = T / 128 + (S < T ? S : T);
     L.header = 0;
     L.prefix = 256;
-    L.tiles = L.prefix + plan_up(static_cast<size_t>(S + 1) * sizeof(int));
+    L.start = L.prefix + plan_up(static_cast<size_t>(S + 1) * sizeof(int));
+    L.tiles = L.start + plan_up(static_cast<size_t>(S) * sizeof(int));
     L.order = L.tiles + plan_up(static_cast<size_t>(L.max_tiles) * sizeof(PackedTile));
     L.vec = L.order + plan_up(static_cast<size_t>(L.max_tiles) * sizeof(int));
     L.dqacc = L.vec + plan_up(static_cast<size_t>(L.max_tiles) * Hq * 256 * sizeof(float));
