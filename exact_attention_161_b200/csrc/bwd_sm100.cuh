@@ -106,8 +106,9 @@ __global__ void __launch_bounds__(256) bwd_prep_packed_kernel(const BwdParams p)
     constexpr int LPR = D / 8, RPP = 256 / LPR, PASSES = 128 / RPP;  // lanes per row, rows per pass
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();  // the plan
-    const int tile = static_cast<int>(blockIdx.x / p.Hq), h = static_cast<int>(blockIdx.x - static_cast<unsigned>(tile) * p.Hq);
-    if (tile >= p.header->n_items) return;
+    const int entry = static_cast<int>(blockIdx.x / p.Hq), h = static_cast<int>(blockIdx.x - static_cast<unsigned>(entry) * p.Hq);
+    if (entry >= p.header->n_items) return;
+    const int tile = p.order[p.header->n_items - 1 - entry];  // the tiles needed first are written last
     const PackedTile t = p.tiles[tile];
     const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
     const int rows = min(128, t.n - t.t * 128);
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(256) bwd_prep_packed_kernel(const BwdParams p)
         a[k] = __ldg(reinterpret_cast<const uint4*>(p.o + off));
         b[k] = __ldg(reinterpret_cast<const uint4*>(p.dout + off));
     }
-    const size_t th = blockIdx.x;
+    const size_t th = static_cast<size_t>(tile) * p.Hq + h;
     float4* z = reinterpret_cast<float4*>(p.dqacc + th * 128 * D) + threadIdx.x;
 #pragma unroll
     for (int k = 0; k < 128 * D / 4 / 256; ++k) z[k * 256] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -750,12 +751,13 @@ template <int D>
 __global__ void __launch_bounds__(256) bwd_dq_store_packed_kernel(const BwdParams p) {
     constexpr int LPR = D / 8, RPP = 256 / LPR, PASSES = 128 / RPP;
     ptx::grid_dependency_wait();
-    const int tile = static_cast<int>(blockIdx.x / p.Hq), h = static_cast<int>(blockIdx.x - static_cast<unsigned>(tile) * p.Hq);
-    if (tile >= p.header->n_items) return;
+    const int entry = static_cast<int>(blockIdx.x / p.Hq), h = static_cast<int>(blockIdx.x - static_cast<unsigned>(entry) * p.Hq);
+    if (entry >= p.header->n_items) return;
+    const int tile = p.order[p.header->n_items - 1 - entry];  // the sums added last are still in L2
     const PackedTile t = p.tiles[tile];
     const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
     const int rows = min(128, t.n - t.t * 128);
-    const float* src = p.dqacc + (static_cast<size_t>(blockIdx.x) * 128 + r0) * D + l * 8;
+    const float* src = p.dqacc + ((static_cast<size_t>(tile) * p.Hq + h) * 128 + r0) * D + l * 8;
     float4 a[PASSES], c[PASSES];
 #pragma unroll
     for (int k = 0; k < PASSES; ++k) {
