@@ -40,7 +40,7 @@ SIGNATURES = {
                               _p]),
     "attn_packed_fwd_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "attn_packed_fwd": (_i, [_p, _p, _p, _l, _l, _l, _p, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p, _sz, _p]),
-    "attn_packed_bwd_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "attn_packed_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "attn_packed_bwd": (_i, [_p, _p, _p, _l, _l, _l, _p, _p, _p, _p, _p, _p, _l, _l, _l, _p, _i, _i, _i, _i, _i, _i,
                              _i, _f, _p, _sz, _p]),
     "attn_chunk_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
@@ -386,8 +386,8 @@ def attn_packed_fwd(q, k, v, cu_seqlens, causal=False, window=0, scale=0.0, o=No
     return _on(dev, stream, call)
 
 
-def packed_bwd_workspace_size(T, num_seqs, Hq, D) -> int:
-    return int(lib.attn_packed_bwd_workspace_size(T, num_seqs, Hq, D))
+def packed_bwd_workspace_size(T, num_seqs, Hq, Hkv, D) -> int:
+    return int(lib.attn_packed_bwd_workspace_size(T, num_seqs, Hq, Hkv, D))
 
 
 def attn_packed_bwd(q, k, v, o, lse, dout, cu_seqlens, causal=False, window=0, scale=0.0, dq=None, dk=None, dv=None,
@@ -411,7 +411,7 @@ def attn_packed_bwd(q, k, v, o, lse, dout, cu_seqlens, causal=False, window=0, s
         (gqp, gqs), (gkp, gks), (gvp, gvs) = _rows(gq, "dq", dev), _rows(gk, "dk", dev), _rows(gv, "dv", dev)
         ws = workspace
         if ws is None:
-            ws = q.new_empty(lib.attn_packed_bwd_workspace_size(T, S, Hq, D), dtype=_U8)
+            ws = q.new_empty(lib.attn_packed_bwd_workspace_size(T, S, Hq, Hkv, D), dtype=_U8)
         _check(lib.attn_packed_bwd(qp, kp, vp, qs, ks, vs, _ptr(o, "o", _BF16, dev), _ptr(lse, "lse", _F32, dev),
                                    _ptr(dout, "dout", _BF16, dev), gqp, gkp, gvp, gqs, gks, gvs,
                                    _ptr(cu_seqlens, "cu_seqlens", _I32, dev), S, T, Hq, Hkv, D, bool(causal), window,

@@ -709,7 +709,8 @@ attn_status launch_packed_bwd(const void* q, const void* k, const void* v, long 
                               long long dqs, long long dks, long long dvs, const int32_t* cu, int S, int T, int Hq,
                               int Hkv, int causal, int window, float scale, void* ws, cudaStream_t stream, int dev) {
     using C = attn::BwdCfg<D>;
-    const attn::BwdPlanLayout L = attn::bwd_plan_layout(T, S, Hq, D);
+    const int G = Hq / Hkv, TT = 128 / G;
+    const attn::BwdPlanLayout L = attn::bwd_plan_layout(T, S, TT, Hkv, D);
     uint8_t* w = static_cast<uint8_t*>(ws);
     attn::PlanParams pl{};
     pl.cu = cu;
@@ -718,9 +719,10 @@ attn_status launch_packed_bwd(const void* q, const void* k, const void* v, long 
     pl.tiles = reinterpret_cast<attn::PackedTile*>(w + L.tiles);
     pl.order = reinterpret_cast<int*>(w + L.order);
     pl.start = reinterpret_cast<int*>(w + L.start);
+    pl.base = reinterpret_cast<int*>(w + L.base);
     pl.S = S;
     pl.T = T;
-    pl.TT = 64;
+    pl.TT = TT;
     pl.Hkv = Hkv;
     pl.causal = causal;
     pl.window = window;
@@ -750,15 +752,14 @@ attn_status launch_packed_bwd(const void* q, const void* k, const void* v, long 
     p.dk_stride = dks;
     p.dv_stride = dvs;
     p.T = T;
-    int sms = 148;
-    CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    p.TT = TT;
     CUtensorMap tq, tk, tv, tdo, tdq;
     attn_status st;
-    if ((st = make_map_tokens(&tq, q, D, Hq, T, qs, 1, 128)) != ATTN_OK) return st;
+    if ((st = make_map_tokens(&tq, q, D, Hq, T, qs, G, TT)) != ATTN_OK) return st;
     if ((st = make_map_tokens(&tk, k, D, Hkv, T, ks, 1, 128)) != ATTN_OK) return st;
     if ((st = make_map_tokens(&tv, v, D, Hkv, T, vs, 1, 128)) != ATTN_OK) return st;
-    if ((st = make_map_tokens(&tdo, dout, D, Hq, T, static_cast<uint64_t>(Hq) * D, 1, 128)) != ATTN_OK) return st;
-    if ((st = make_map_2d_f32(&tdq, p.dqacc, D, static_cast<uint64_t>(L.max_tiles) * Hq * 128)) != ATTN_OK) return st;
+    if ((st = make_map_tokens(&tdo, dout, D, Hq, T, static_cast<uint64_t>(Hq) * D, G, TT)) != ATTN_OK) return st;
+    if ((st = make_map_2d_f32(&tdq, p.dqacc, D, static_cast<uint64_t>(L.max_q_tiles) * Hkv * 128)) != ATTN_OK) return st;
     if ((st = ensure_smem(attn::attn_bwd_kernel<D, true>, C::SMEM_BYTES, dev)) != ATTN_OK) return st;
     cudaLaunchAttribute attr[1];
     const unsigned pass_grid = static_cast<unsigned>(L.max_tiles * Hq);  // the device knows how many tiles there are
@@ -791,10 +792,9 @@ attn_status check_rows(const char* name, const void* ptr, long long stride, int 
         return fail(ATTN_ERR_INVALID_ARG, "%s: token stride %lld must be a multiple of 8, >= heads * D and < 2^38", name, stride);
     return ATTN_OK;
 }
-// Overflow limits of the device's 32-bit indices: items (blocks and parts for every K/V head), and
-// rows of packed tiles.
-bool too_many_rows(long long T, long long S, int heads) {
-    return static_cast<double>(T / 128 + (S < T ? S : T) + 1) * 128 * heads >= 2147483648.0;
+// Overflow limit of the device's 32-bit indices: rows of query tiles.
+bool too_many_rows(long long T, long long S, int Hq, int Hkv) {
+    return static_cast<double>(T / (128 / (Hq / Hkv)) + (S < T ? S : T) + 1) * 128 * Hkv >= 2147483648.0;
 }
 
 // Forgets the cached device addresses of the no-alloc decode's array (defined with it below).
@@ -1134,7 +1134,7 @@ attn_status attn_packed_fwd(const void* q, const void* k, const void* v, int64_t
     if (!aligned16(o) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) ||
         (reinterpret_cast<uintptr_t>(lse) & 3u))
         return fail(ATTN_ERR_INVALID_ARG, "misaligned pointer (tensors 16-byte, int32/fp32 arrays 4-byte)");
-    if (too_many_rows(T, num_seqs, Hq)) return fail(ATTN_ERR_UNSUPPORTED, "too many rows: (T + 128 num_seqs) * Hq must be < 2^31");
+    if (too_many_rows(T, num_seqs, Hq, Hkv)) return fail(ATTN_ERR_UNSUPPORTED, "too many rows: 128 * Hkv * (T / floor(128 Hkv / Hq) + num_seqs) must be < 2^31");
     const size_t need = attn_packed_fwd_workspace_size(T, num_seqs, Hq, Hkv, D);
     if (workspace_bytes < need)
         return fail(ATTN_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
@@ -1162,9 +1162,9 @@ attn_status attn_packed_fwd(const void* q, const void* k, const void* v, int64_t
     return D == 64 ? launch_packed<64, false>(c, s, dev) : launch_packed<128, false>(c, s, dev);
 }
 
-size_t attn_packed_bwd_workspace_size(int T, int num_seqs, int Hq, int D) {
-    if (T < 1 || num_seqs < 1 || Hq < 1 || D < 1) return 0;
-    return attn::bwd_plan_layout(T, num_seqs, Hq, D).total;
+size_t attn_packed_bwd_workspace_size(int T, int num_seqs, int Hq, int Hkv, int D) {
+    if (T < 1 || num_seqs < 1 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0 || Hq / Hkv > 128) return 0;
+    return attn::bwd_plan_layout(T, num_seqs, 128 / (Hq / Hkv), Hkv, D).total;
 }
 
 attn_status attn_packed_bwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
@@ -1187,8 +1187,8 @@ attn_status attn_packed_bwd(const void* q, const void* k, const void* v, int64_t
     if (!aligned16(o) || !aligned16(dout) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) ||
         (reinterpret_cast<uintptr_t>(lse) & 3u))
         return fail(ATTN_ERR_INVALID_ARG, "misaligned pointer (tensors 16-byte, int32/fp32 arrays 4-byte)");
-    if (too_many_rows(T, num_seqs, Hq)) return fail(ATTN_ERR_UNSUPPORTED, "too many rows: (T + 128 num_seqs) * Hq must be < 2^31");
-    const size_t need = attn_packed_bwd_workspace_size(T, num_seqs, Hq, D);
+    if (too_many_rows(T, num_seqs, Hq, Hkv)) return fail(ATTN_ERR_UNSUPPORTED, "too many rows: 128 * Hkv * (T / floor(128 Hkv / Hq) + num_seqs) must be < 2^31");
+    const size_t need = attn_packed_bwd_workspace_size(T, num_seqs, Hq, Hkv, D);
     if (workspace_bytes < need)
         return fail(ATTN_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
     if (scale <= 0.f) scale = 1.0f / std::sqrt(static_cast<float>(D));
@@ -1242,7 +1242,7 @@ attn_status attn_chunk_paged(const void* q, const void* k_new, const void* v_new
         (reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
         (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
         return fail(ATTN_ERR_INVALID_ARG, "misaligned pointer (tensors 16-byte, int32/fp32 arrays 4-byte)");
-    if (too_many_rows(T, num_seqs, Hq)) return fail(ATTN_ERR_UNSUPPORTED, "too many rows: (T + 128 num_seqs) * Hq must be < 2^31");
+    if (too_many_rows(T, num_seqs, Hq, Hkv)) return fail(ATTN_ERR_UNSUPPORTED, "too many rows: 128 * Hkv * (T / floor(128 Hkv / Hq) + num_seqs) must be < 2^31");
     const size_t need = attn_chunk_workspace_size(T, num_seqs, max_blocks_per_seq, page_size, Hq, Hkv, D);
     if (workspace_bytes < need)
         return fail(ATTN_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);

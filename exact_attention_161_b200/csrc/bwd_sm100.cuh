@@ -44,14 +44,16 @@ struct BwdParams {
     int causal, window;
     float scale, scale_log2;
     int debug_drop_copy;        // test hook: CTA 0 skips its first Q / dO copy (see attn.h)
-    // Packed sequences (the kernels' kPacked forms): o and dout are [T, Hq, D], lse is [Hq, T]; the
-    // 128-row tiles of all sequences are numbered one behind the other, vec is [tiles, Hq, 2, 128] and
-    // dqacc [tiles, Hq, 128, D]; the gradients' rows are dq_stride, dk_stride, dv_stride elements apart.
+    // Packed sequences (the kernels' kPacked forms): o and dout are [T, Hq, D], lse is [Hq, T]. A query
+    // tile's 128 rows are TT tokens times the G query heads of a K/V head (row = token * G + head), as in
+    // attn_packed_kernel; those of all sequences are numbered one behind the other, vec is [query tiles, Hkv,
+    // 2, 128] and dqacc [query tiles, Hkv, 128, D]. The gradients' rows are dq_stride, dk_stride, dv_stride
+    // elements apart.
     const PlanHeader* header;
-    const PackedTile* tiles;
-    const int* order;           // tile numbers, most visible query tiles first
+    const PackedTile* tiles;    // of 128 keys
+    const int* order;           // tile numbers, longest sequence first
     long long dq_stride, dk_stride, dv_stride;
-    int T;
+    int T, TT;
 };
 
 // Per query row: -D_i = -(dO_i . O_i) and -LSE_i * log2(e), stored negated so that the kernels add
@@ -99,8 +101,15 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const BwdParams p) {
     }
 }
 
-// The same for packed sequences, a block per (tile, query head). All of a thread's loads are issued
-// before the first is used.
+// Row of token `i` of a key tile's 128 tokens and query head h in the query tiles' arrays.
+__device__ __forceinline__ size_t packed_query_row(const BwdParams& p, const PackedTile& t, int i, int h, int G) {
+    const int token = t.t * 128 + i, q_tile = token / p.TT, g = h / G;
+    return (static_cast<size_t>(t.base + q_tile) * p.Hkv + g) * 128 + (token - q_tile * p.TT) * G + (h - g * G);
+}
+
+// The same for packed sequences, a block per (128 tokens of a sequence, query head). All of a thread's loads
+// are issued before the first is used. The rows of a query tile that no token has are left as they are:
+// nothing reads them but by selection.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_prep_packed_kernel(const BwdParams p) {
     constexpr int LPR = D / 8, RPP = 256 / LPR, PASSES = 128 / RPP;  // lanes per row, rows per pass
@@ -108,9 +117,8 @@ __global__ void __launch_bounds__(256) bwd_prep_packed_kernel(const BwdParams p)
     ptx::grid_dependency_wait();  // the plan
     const int entry = static_cast<int>(blockIdx.x / p.Hq), h = static_cast<int>(blockIdx.x - static_cast<unsigned>(entry) * p.Hq);
     if (entry >= p.header->n_items) return;
-    const int tile = p.order[p.header->n_items - 1 - entry];  // the tiles needed first are written last
-    const PackedTile t = p.tiles[tile];
-    const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+    const PackedTile t = p.tiles[p.order[p.header->n_items - 1 - entry]];  // the tiles needed first are written last
+    const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR, G = p.Hq / p.Hkv;
     const int rows = min(128, t.n - t.t * 128);
     const size_t token0 = static_cast<size_t>(t.row0) + t.t * 128;
     uint4 a[PASSES], b[PASSES];
@@ -123,10 +131,6 @@ __global__ void __launch_bounds__(256) bwd_prep_packed_kernel(const BwdParams p)
         a[k] = __ldg(reinterpret_cast<const uint4*>(p.o + off));
         b[k] = __ldg(reinterpret_cast<const uint4*>(p.dout + off));
     }
-    const size_t th = static_cast<size_t>(tile) * p.Hq + h;
-    float4* z = reinterpret_cast<float4*>(p.dqacc + th * 128 * D) + threadIdx.x;
-#pragma unroll
-    for (int k = 0; k < 128 * D / 4 / 256; ++k) z[k * 256] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < PASSES; ++k) {
         const int i = r0 + k * RPP;
@@ -139,10 +143,15 @@ __global__ void __launch_bounds__(256) bwd_prep_packed_kernel(const BwdParams p)
         }
 #pragma unroll
         for (int m = LPR / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+        if (i >= rows) continue;
+        const size_t row = packed_query_row(p, t, i, h, G);
+        float4* z = reinterpret_cast<float4*>(p.dqacc + row * D) + l;
+        z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+        z[LPR] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (l == 0) {
-            float* v = p.vec + th * 256 + i;
-            v[0] = i < rows ? -p.lse[static_cast<size_t>(h) * p.T + token0 + i] * kLog2e : -INFINITY;
-            v[128] = i < rows ? -acc : 0.f;
+            float* v = p.vec + (row >> 7) * 256 + (row & 127);
+            v[0] = -p.lse[static_cast<size_t>(h) * p.T + token0 + i] * kLog2e;
+            v[128] = -acc;
         }
     }
 }
@@ -298,11 +307,13 @@ __device__ __forceinline__ uint32_t dq_box(int cg, int qw, const uint8_t* sQ, co
 // issuing it earlier in the step gains nothing.
 //
 // kPacked: the CTA's key tile is the (block number / Hkv)-th of the plan's order, of a sequence of N
-// tokens whose rows start at row0 of the packed tensors. Rows behind the sequence's end belong to
-// another sequence or to nobody and may hold NaN: such queries and keys get P = dS = 0 by selection, and
-// where they are summed over (dV and dK over queries, dQ over keys) the product stops at the last
-// 16-row slice with a valid row, whose other rows are set to zero in shared memory by the
-// elementwise warps before P^T (dO) and dS^T (Q, K) are handed over.
+// tokens whose rows start at row0 of the packed tensors; a step is one query tile of TT tokens times the G
+// heads (the unpacked kernel walks 128 tokens of one head after the other: at four heads to a K/V head the
+// ends of 16 documents of 705 tokens on average then leave 8% more rows empty). Rows behind the sequence's
+// end belong to another sequence or to nobody and may hold NaN: such queries and keys get P = dS = 0 by
+// selection, and where they are summed over (dV and dK over queries, dQ over keys) the product stops at the
+// last 16-row slice with a valid row, whose other rows are set to zero in shared memory by the elementwise
+// warps before P^T (dO) and dS^T (Q, K) are handed over.
 template <int D, bool kPacked = false>
 __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -323,7 +334,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.Hq / p.Hkv;
     int ib, ie, j0, g, b = 0;
-    int N = p.N, row0 = 0, tile0 = 0;  // packed: the sequence's tokens, first row and first tile
+    int N = p.N, row0 = 0, tile0 = 0;  // packed: the sequence's tokens, first row and first query tile
     if constexpr (kPacked) {
         ptx::grid_launch_dependents();
         ptx::grid_dependency_wait();  // the plan and the prep pass
@@ -335,7 +346,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         row0 = tile.row0;
         tile0 = tile.base;
         j0 = tile.t * 128;
-        query_tiles(tile.t, N, p.causal, p.window, ib, ie);
+        query_tiles(tile.t, N, p.TT, p.causal, p.window, ib, ie);
     } else {
         const int groups = p.B * p.Hkv;
         const int jt = static_cast<int>(blockIdx.x / groups);
@@ -346,7 +357,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         query_tiles_for_keys(j0, p.N, p.causal, p.window, ib, ie);
     }
     const int per_head = max(0, ie - ib);
-    const int T = G * per_head;  // steps
+    const int heads = kPacked ? 1 : G;  // steps per query tile
+    auto query_rows = [&](int qt) { return kPacked ? min(p.TT, N - qt * p.TT) * G : 128; };  // of query tile qt
+    const int T = heads * per_head;  // steps
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(&bar->fixed_loaded, 1);
@@ -391,18 +404,19 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             for (int t = 0; t < T && ok; ++t) {
                 const int s = t & 1;
                 if (t >= 2 && !ptx::mbar_wait(&bar->empty[s], ((t >> 1) - 1) & 1, abort_flag)) { ok = false; break; }
-                const int qt = ie - 1 - t / G, h = g * G + t % G;
+                const int qt = ie - 1 - t / heads, h = g * G + t % heads;
                 const int zq = b * p.Hq + h;
-                ptx::mbar_arrive_expect_tx(&bar->full[s], 2 * C::TILE_BYTES + C::VEC_BYTES);
+                const uint32_t tile_bytes = kPacked ? G * p.TT * D * 2 : C::TILE_BYTES;
+                ptx::mbar_arrive_expect_tx(&bar->full[s], 2 * tile_bytes + C::VEC_BYTES);
                 if (!(p.debug_drop_copy && t == 0 && blockIdx.x == 0)) {
-                    const int c1 = kPacked ? h : qt * 128, c2 = kPacked ? row0 + qt * 128 : zq;
+                    const int c1 = kPacked ? h : qt * 128, c2 = kPacked ? row0 + qt * p.TT : zq;
                     for (int r = 0; r < C::NREG; ++r) {
                         ptx::tma_load_3d(sQ + s * C::TILE_BYTES + r * C::REGION_BYTES, &tm_q, &bar->full[s], r * 64, c1,
                                          c2);
                         ptx::tma_load_3d(sDO + s * C::TILE_BYTES + r * C::REGION_BYTES, &tm_do, &bar->full[s], r * 64, c1,
                                          c2);
                     }
-                    const size_t vec_tile = kPacked ? static_cast<size_t>(tile0 + qt) * p.Hq + h
+                    const size_t vec_tile = kPacked ? static_cast<size_t>(tile0 + qt) * p.Hkv + g
                                                     : static_cast<size_t>(zq) * p.ntiles + qt;
                     ptx::bulk_load(sVec + s * 256, p.vec + vec_tile * 256, C::VEC_BYTES, &bar->full[s]);
                 }
@@ -459,7 +473,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             };
             // 16-row slices of step t's query tile and of the key tile that hold a row of the sequence
             auto query_slices = [&](int t) {
-                return kPacked ? min(8, (N - (ie - 1 - t / G) * 128 + 15) >> 4) : 8;
+                return kPacked ? (query_rows(ie - 1 - t) + 15) >> 4 : 8;
             };
             const int key_slices = kPacked ? min(8, (N - j0 + 15) >> 4) : 8;
             // dV += P^T dO (M = 128 keys, N = D, K = 128 queries; P^T packed in TMEM)
@@ -549,10 +563,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
             bool ok = true;
             for (int t = 0; t < T; ++t) {
                 const int s = t & 1;
-                const int qt = ie - 1 - t / G, h = g * G + t % G;
+                const int qt = ie - 1 - t / heads, h = g * G + t % heads;
                 if (!ptx::mbar_wait(&bar->staged[s], (t >> 1) & 1, abort_flag)) { ok = false; break; }
-                const int acc_row = (kPacked ? (tile0 + qt) * p.Hq + h : (b * p.Hq + h) * p.ntiles + qt) * 128;
-                const int boxes = kPacked ? min(4, (N - qt * 128 + 31) >> 5) : 4;  // 32-row boxes with a valid row
+                const int acc_row = (kPacked ? (tile0 + qt) * p.Hkv + g : (b * p.Hq + h) * p.ntiles + qt) * 128;
+                const int boxes = kPacked ? (query_rows(qt) + 31) >> 5 : 4;  // 32-row boxes with a valid row
 #pragma unroll 1
                 for (int cg = 0; cg < D / 32; ++cg)
 #pragma unroll
@@ -582,8 +596,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
         bool ok = true;
         for (int t = 0; ok && t < T; ++t) {
             const int s = t & 1;
-            const int qt = ie - 1 - t / G;
-            const int c0 = qt * 128 + 32 * cg;  // first query of this group's columns
+            const int qt = ie - 1 - t / heads;
+            const int c0 = qt * 128 + 32 * cg;  // unpacked: first query of this group's columns
             if (!ptx::mbar_wait(&bar->full[s], (t >> 1) & 1, abort_flag)) { ok = false; break; }
             if (!ptx::mbar_wait(&bar->s_full, t & 1, abort_flag)) { ok = false; break; }
             ptx::tc_fence_after();
@@ -595,12 +609,18 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                 probs32_cols(sv, p.scale_log2, vec, pr);
             }
             // query qpos sees this key iff qpos >= key (causal) and qpos - key < window
-            const int lo = p.causal ? key - c0 : -1;
-            int hi = p.window > 0 ? key + p.window - 1 - c0 : 32;
+            int lo, hi;
             bool past_end = false;  // packed: a query column or the key row lies behind the sequence
             if constexpr (kPacked) {
-                past_end = key >= N || c0 + 32 > N;
-                if (past_end) hi = key >= N ? -1 : min(hi, N - 1 - c0);
+                // column c of the tile is token qt * TT + c / G
+                const int first = qt * p.TT, rows = query_rows(qt);
+                lo = p.causal ? min(max(key - first, 0), p.TT) * G - 32 * cg : 0;
+                hi = p.window > 0 ? min(max(key + p.window - first, 0), p.TT) * G - 1 : 127;
+                past_end = key >= N || 32 * cg + 32 > rows;
+                hi = key >= N ? -1 : min(hi, rows - 1) - 32 * cg;
+            } else {
+                lo = p.causal ? key - c0 : -1;
+                hi = p.window > 0 ? key + p.window - 1 - c0 : 32;
             }
             if (lo > 0 || hi < 31) mask32(pr, lo, hi);
             if constexpr (kPacked) {
@@ -611,7 +631,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
                     for (int e = threadIdx.x; e < chunks * C::NREG; e += C::EW_THREADS)
                         ptx::st_shared_v4(base + (e / chunks) * C::REGION_BYTES + (e % chunks) * 16, 0, 0, 0, 0);
                 };
-                const int q_rows = N - qt * 128, k_rows = N - j0;
+                const int q_rows = query_rows(qt), k_rows = N - j0;
                 const bool q_tail = q_rows < 128 && (q_rows & 15), k_tail = t == 0 && k_rows < 128 && (k_rows & 15);
                 if (q_tail) {
                     zero_rows(sQ + s * C::TILE_BYTES, q_rows);
@@ -746,26 +766,25 @@ __global__ void __launch_bounds__(256) bwd_dq_store_kernel(const BwdParams p) {
     }
 }
 
-// The same for packed sequences, a block per (tile, query head), rows dq_stride elements apart.
+// The same for packed sequences, a block per (128 tokens of a sequence, query head), rows dq_stride elements
+// apart.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_dq_store_packed_kernel(const BwdParams p) {
     constexpr int LPR = D / 8, RPP = 256 / LPR, PASSES = 128 / RPP;
     ptx::grid_dependency_wait();
     const int entry = static_cast<int>(blockIdx.x / p.Hq), h = static_cast<int>(blockIdx.x - static_cast<unsigned>(entry) * p.Hq);
     if (entry >= p.header->n_items) return;
-    const int tile = p.order[p.header->n_items - 1 - entry];  // the sums added last are still in L2
-    const PackedTile t = p.tiles[tile];
-    const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR;
+    const PackedTile t = p.tiles[p.order[p.header->n_items - 1 - entry]];  // the sums added last are still in L2
+    const int l = threadIdx.x % LPR, r0 = threadIdx.x / LPR, G = p.Hq / p.Hkv;
     const int rows = min(128, t.n - t.t * 128);
-    const float* src = p.dqacc + ((static_cast<size_t>(tile) * p.Hq + h) * 128 + r0) * D + l * 8;
     float4 a[PASSES], c[PASSES];
 #pragma unroll
     for (int k = 0; k < PASSES; ++k) {
-        const float4* x = reinterpret_cast<const float4*>(src + static_cast<size_t>(k) * RPP * D);
-        if (r0 + k * RPP < rows) {
-            a[k] = __ldcs(x);
-            c[k] = __ldcs(x + 1);
-        }
+        const int i = r0 + k * RPP;
+        if (i >= rows) continue;
+        const float4* x = reinterpret_cast<const float4*>(p.dqacc + packed_query_row(p, t, i, h, G) * D + l * 8);
+        a[k] = __ldcs(x);
+        c[k] = __ldcs(x + 1);
     }
     __nv_bfloat16* dst = p.dq + (static_cast<size_t>(t.row0) + t.t * 128 + r0) * p.dq_stride + h * D + l * 8;
 #pragma unroll

@@ -46,6 +46,7 @@ struct PlanParams {
     PackedTile* tiles;        // backward: natural order
     int* order;               // backward: tile numbers, longest sequence first
     int* start;               // backward: [S] where each sequence's tiles stand in the order
+    int* base;                // backward: [S] query tiles of the sequences before each
     int S, T, TT, Hkv, causal, window;
     int max_len;              // paged: tokens a block-table row can hold
 };
@@ -106,22 +107,29 @@ __device__ void build_plan(const PlanParams& p) {
         s_slots = 0;
         s_load[0] = s_load[1] = 0;
     }
-    int carry = 0, bad = 0;
+    int carry = 0, bad = 0, q_carry = 0;
     for (int base = 0; base < p.S; base += kPlanThreads) {
         const int s = base + tid;
-        int blocks = 0;
+        int blocks = 0, q_tiles = 0;
         if (s < p.S) {
             const int a = p.cu[s], b = p.cu[s + 1];
             if (a < 0 || b < a || b > p.T)
                 bad = 1;
-            else
+            else {
                 blocks = plan_ceil(b - a, tok);
+                q_tiles = plan_ceil(b - a, p.TT);
+            }
         }
         int total;
         const int at = plan_scan(blocks, s_warp, total);
         if (s < p.S) pre[s] = carry + at;
         // T < 2^30 bounds the sum of valid offsets; with invalid ones it may pass 2^31, and the list is not built
         carry += total;
+        if constexpr (kBwd) {
+            const int q_at = plan_scan(q_tiles, s_warp, total);
+            if (s < p.S) p.base[s] = q_carry + q_at;
+            q_carry += total;
+        }
     }
     bad = __syncthreads_or(bad);
     const int n_blocks = bad ? 0 : carry;
@@ -179,8 +187,8 @@ __device__ void build_plan(const PlanParams& p) {
             PackedTile t;
             t.row0 = p.cu[s];
             t.n = p.cu[s + 1] - t.row0;
-            t.base = pre[s];
-            t.t = b - t.base;
+            t.base = p.base[s];
+            t.t = b - pre[s];
             p.tiles[b] = t;
             p.order[p.start[s] + t.t] = b;
         }

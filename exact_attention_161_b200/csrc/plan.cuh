@@ -55,8 +55,8 @@ ATTN_HD int item_part(const PackedItem& x) { return (x.meta >> 10) & 1023; }
 ATTN_HD int item_parts(const PackedItem& x) { return ((x.meta >> 20) & 1023) + 1; }
 ATTN_HD int make_meta(int n_tok, int part, int parts) { return n_tok | (part << 10) | ((parts - 1) << 20); }
 
-// One 128-row tile of a packed sequence, for the backward: rows [row0 + 128 t, ...) of a sequence
-// of n rows that starts at row0; base is the number of the sequence's first tile.
+// One tile of 128 keys of a packed sequence, for the backward: rows [row0 + 128 t, ...) of a sequence of n
+// rows that starts at row0; base is the number of the sequence's first query tile (of TT tokens).
 struct PackedTile {
     int row0, n, t, base;
 };
@@ -82,12 +82,12 @@ ATTN_HD KeyTiles key_tiles(int first, int last, int kv_len, int causal, int wind
     return t;
 }
 
-// Query tiles of a sequence of n tokens that see some key of key tile t: [ib, ie).
-ATTN_HD void query_tiles(int t, int n, int causal, int window, int& ib, int& ie) {
-    ib = causal ? t : 0;
-    ie = plan_ceil(n, 128);
+// Query tiles (TT tokens each) of a sequence of n tokens that see some key of key tile t: [ib, ie).
+ATTN_HD void query_tiles(int t, int n, int TT, int causal, int window, int& ib, int& ie) {
+    ib = causal ? t * 128 / TT : 0;
+    ie = plan_ceil(n, TT);
     // the last query that sees the tile's last key is window - 1 rows after it
-    if (window > 0 && window < n) ie = plan_min(ie, (t * 128 + 127 + window - 1) / 128 + 1);
+    if (window > 0 && window < n) ie = plan_min(ie, (t * 128 + 127 + window - 1) / TT + 1);
 }
 
 // What `tiles` key tiles cost, in steps of a CTA (one key tile for both query tiles): a block of one
@@ -149,22 +149,26 @@ ATTN_HD PlanLayout plan_layout(long long T, long long S, int TT, long long max_k
     return L;
 }
 
-// Byte offsets of a backward plan and its arrays: tiles <= T / 128 + S, each of 128 padded rows.
+// Byte offsets of a backward plan and its arrays: key tiles <= T / 128 + S, and query tiles of 128 rows
+// (TT tokens times the query heads of a K/V head) for each K/V head, <= T / TT + S.
 struct BwdPlanLayout {
-    size_t header, prefix, start, tiles, order, vec, dqacc, total;
-    long long max_tiles;
+    size_t header, prefix, start, base, tiles, order, vec, dqacc, total;
+    long long max_tiles, max_q_tiles;
 };
-ATTN_HD BwdPlanLayout bwd_plan_layout(long long T, long long S, int Hq, int D) {
+ATTN_HD BwdPlanLayout bwd_plan_layout(long long T, long long S, int TT, int Hkv, int D) {
     BwdPlanLayout L;
     L.max_tiles = T / 128 + (S < T ? S : T);
+    L.max_q_tiles = T / TT + (S < T ? S : T);
     L.header = 0;
     L.prefix = 256;
     L.start = L.prefix + plan_up(static_cast<size_t>(S + 1) * sizeof(int));
-    L.tiles = L.start + plan_up(static_cast<size_t>(S) * sizeof(int));
+    L.base = L.start + plan_up(static_cast<size_t>(S) * sizeof(int));
+    L.tiles = L.base + plan_up(static_cast<size_t>(S) * sizeof(int));
     L.order = L.tiles + plan_up(static_cast<size_t>(L.max_tiles) * sizeof(PackedTile));
     L.vec = L.order + plan_up(static_cast<size_t>(L.max_tiles) * sizeof(int));
-    L.dqacc = L.vec + plan_up(static_cast<size_t>(L.max_tiles) * Hq * 256 * sizeof(float));
-    L.total = L.dqacc + plan_up(static_cast<size_t>(L.max_tiles) * Hq * 128 * D * sizeof(float));
+    const size_t rows = static_cast<size_t>(L.max_q_tiles) * Hkv * 128;
+    L.dqacc = L.vec + plan_up(rows * 2 * sizeof(float));
+    L.total = L.dqacc + plan_up(rows * D * sizeof(float));
     return L;
 }
 

@@ -301,7 +301,8 @@ attn_status attn_decode_paged_noalloc(const void* q, const void* k_pages, const 
  *          on the GPU, and captured graphs that may run side by side, need their own.
  * Within a sequence K and V must be finite. Values are bf16; scores, softmax statistics and sums are
  * fp32, P is rounded to bf16 for its product as in attn_fwd. Constraints: D in {64, 128},
- * Hq / Hkv <= 128 (else ATTN_ERR_UNSUPPORTED), (T + 128 * num_seqs) * Hq < 2^31. Nothing is allocated or
+ * Hq / Hkv <= 128 (else ATTN_ERR_UNSUPPORTED), 128 * Hkv * (T / floor(128 * Hkv / Hq) + num_seqs) < 2^31
+ * (about T * Hq). Nothing is allocated or
  * cached, and the calls can be captured into a graph and replayed with other lengths.
  */
 
@@ -329,10 +330,11 @@ attn_status attn_packed_fwd(const void* q, const void* k, const void* v, int64_t
 
 /*
  * attn_packed_bwd_workspace_size -- bytes of workspace attn_packed_bwd needs: the tile list, and fp32
- * (-LSE*log2 e, -D_i) and dq sums (D values) per query row padded to 128-row tiles of each sequence.
+ * (-LSE*log2 e, -D_i) and dq sums (D values) per query row, padded to tiles of 128 rows (floor(128 * Hkv / Hq)
+ * tokens times Hq / Hkv heads) in each sequence.
  * 0 for invalid sizes.
  */
-size_t attn_packed_bwd_workspace_size(int T, int num_seqs, int Hq, int D);
+size_t attn_packed_bwd_workspace_size(int T, int num_seqs, int Hq, int Hkv, int D);
 
 /*
  * attn_packed_bwd -- gradients of L = sum(O * dout) for attn_packed_fwd, with the formulas of attn_bwd.

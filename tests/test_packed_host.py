@@ -28,7 +28,7 @@ def plan(tmp_path_factory):
     src.write_text('#include "plan.cuh"\nusing namespace attn;\nextern "C" {\n'
                    'void keys(int f, int l, int m, int c, int w, int* o) { KeyTiles t = key_tiles(f, l, m, c, w);'
                    ' o[0] = t.jb; o[1] = t.n; }\n'
-                   'void queries(int t, int n, int c, int w, int* o) { query_tiles(t, n, c, w, o[0], o[1]); }\n'
+                   'void queries(int t, int n, int q, int c, int w, int* o) { query_tiles(t, n, q, c, w, o[0], o[1]); }\n'
                    'int limit(long long t, int h) { return plan_limit(t, h); }\n'
                    'int parts(int t, int l) { return plan_parts(t, l); }\n'
                    'void part(int t, int p, int i, int* o) { plan_part(t, p, i, o[0], o[1]); }\n'
@@ -36,17 +36,18 @@ def plan(tmp_path_factory):
                    ' { return plan_layout(T, S, TT, m, h, 128).max_slots; }\n'
                    'long long items(long long T, long long S, int TT, long long m, int h)'
                    ' { return plan_layout(T, S, TT, m, h, 128).max_items; }\n'
-                   'long long tiles(long long T, long long S) { return bwd_plan_layout(T, S, 1, 64).max_tiles; }\n'
+                   'long long tiles(long long T, long long S) { return bwd_plan_layout(T, S, 128, 1, 64).max_tiles; }\n'
+                   'long long q_tiles(long long T, long long S, int TT)'
+                   ' { return bwd_plan_layout(T, S, TT, 1, 64).max_q_tiles; }\n'
                    'int meta(int n, int p, int q) { PackedItem x; x.meta = make_meta(n, p, q);'
                    ' return item_tokens(x) == n && item_part(x) == p && item_parts(x) == q; }\n}\n')
     lib = d / "libplan.so"
     subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I",
                     os.path.join(ROOT, "exact_attention_161_b200", "csrc"), str(src), "-o", str(lib)], check=True)
     p = ctypes.CDLL(str(lib))
-    for f in (p.slots, p.items, p.tiles):
+    for f, n in ((p.slots, 5), (p.items, 5), (p.tiles, 2), (p.q_tiles, 3)):
         f.restype = ctypes.c_longlong
-        f.argtypes = [ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong, ctypes.c_int][
-            :2 if f is p.tiles else 5]
+        f.argtypes = [ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong, ctypes.c_int][:n]
     p.limit.argtypes = [ctypes.c_longlong, ctypes.c_int]
     return p
 
@@ -71,11 +72,11 @@ def test_visible_tiles_against_brute_force(plan, causal, window):
                 tiles = {j // 128 for j in range(m) if any(sees(off + i, j, m) for i in range(first, last + 1))}
                 jb, cnt = _pair(plan.keys, off + first, off + last, m, causal, window)
                 assert set(range(jb, jb + cnt)) == tiles, (n, m, first, last)
-    for n in (1, 100, 128, 129, 500, 1000):
+    for n, TT in [(1, 128), (100, 128), (128, 32), (129, 42), (500, 128), (500, 32), (500, 25), (300, 1), (1000, 64)]:
         for t in range((n + 127) // 128):
-            tiles = {i // 128 for i in range(n) for j in range(t * 128, min(n, t * 128 + 128)) if sees(i, j, n)}
-            ib, ie = _pair(plan.queries, t, n, causal, window)
-            assert set(range(ib, ie)) == tiles, (n, t)
+            tiles = {i // TT for i in range(n) for j in range(t * 128, min(n, t * 128 + 128)) if sees(i, j, n)}
+            ib, ie = _pair(plan.queries, t, n, TT, causal, window)
+            assert set(range(ib, ie)) == tiles, (n, t, TT)
 
 
 @pytest.mark.parametrize("Hkv", [1, 2, 8, 32])
@@ -95,9 +96,10 @@ def test_work_list_fits_the_workspace(plan, TT, Hkv):
         max_keys = max(c + n for c, n in zip(ctx, new))
         if trial % 2 == 0:
             max_keys = T  # packed: a sequence may hold every token
-        blocks, tiles_bwd = [], 0
+        blocks, tiles_bwd, q_tiles = [], 0, 0
         for c, n in zip(ctx, new):
             tiles_bwd += -(-n // 128)
+            q_tiles += -(-n // TT)
             for first in range(0, n, 2 * TT):
                 last = min(n, first + 2 * TT) - 1
                 blocks.append(_pair(plan.keys, c + first, c + last, c + n, 1, 0)[1])
@@ -113,7 +115,7 @@ def test_work_list_fits_the_workspace(plan, TT, Hkv):
             slots += p if p > 1 else 0
         assert slots <= plan.slots(T, S, TT, max_keys, Hkv)
         assert items <= plan.items(T, S, TT, max_keys, Hkv)
-        assert tiles_bwd <= plan.tiles(T, S)
+        assert tiles_bwd <= plan.tiles(T, S) and q_tiles <= plan.q_tiles(T, S, TT)
 
 
 FAKE, MISALIGNED = ctypes.c_void_p(0x10000), ctypes.c_void_p(0x10008)
@@ -144,7 +146,7 @@ def test_packed_fwd_refusals(api, kw, expect):
 
 def _bwd(api, q=FAKE, k=FAKE, lse=FAKE, dout=FAKE, dq=FAKE, dk=FAKE, cu=FAKE, T=100, S=3, Hq=8, Hkv=2, D=128, causal=1,
          window=0, scale=0.0, qs=None, dks=None, ws=FAKE, ws_bytes=None):
-    ws_bytes = api.packed_bwd_workspace_size(T, S, Hq, D) if ws_bytes is None else ws_bytes
+    ws_bytes = api.packed_bwd_workspace_size(T, S, Hq, Hkv, D) if ws_bytes is None else ws_bytes
     return api.lib.attn_packed_bwd(q, k, FAKE, Hq * D if qs is None else qs, Hkv * D, Hkv * D, FAKE, lse, dout, dq, dk,
                                    FAKE, Hq * D, Hkv * D if dks is None else dks, Hkv * D, cu, S, T, Hq, Hkv, D, causal,
                                    window, scale, ws, ws_bytes, None)
@@ -211,10 +213,11 @@ def test_workspace_sizes(api):
     assert api.packed_fwd_workspace_size(1 << 20, 4, 32, 8, 128) < 100 << 20
     assert api.chunk_workspace_size(64, 64, 1024, 16, 32, 8, 128) < 100 << 20
     # backward: per padded row and head two fp32 vectors and D fp32 sums
-    assert api.packed_bwd_workspace_size(128, 1, 4, 128) == 5 * 256 + 2 * 4 * 128 * (2 + 128) * 4
+    # (128 tokens of 4 heads on 2 K/V heads: two tiles of 64 tokens, and one for the sequence's end)
+    assert api.packed_bwd_workspace_size(128, 1, 4, 2, 128) == 6 * 256 + 3 * 2 * 128 * (2 + 128) * 4
     for bad in ((0, 1, 8, 2, 128), (10, 0, 8, 2, 128), (10, 1, 8, 3, 128), (10, 1, 256, 1, 128)):
         assert api.packed_fwd_workspace_size(*bad) == 0
-    assert api.packed_bwd_workspace_size(10, 0, 8, 128) == 0 and api.chunk_workspace_size(1, 1, 0, 16, 8, 2, 128) == 0
+    assert api.packed_bwd_workspace_size(10, 0, 8, 2, 128) == 0 and api.packed_bwd_workspace_size(9, 1, 8, 3, 128) == 0 and api.chunk_workspace_size(1, 1, 0, 16, 8, 2, 128) == 0
 
 
 def test_binding_refuses_what_is_not_on_the_gpu(api):
