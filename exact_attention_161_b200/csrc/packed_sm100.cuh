@@ -97,7 +97,7 @@ __device__ void build_plan(const PlanParams& p) {
     __shared__ int s_prefix[kPlanSmemSeqs + 1];
     __shared__ int s_warp[33];
     __shared__ unsigned long long s_sum;
-    __shared__ int s_max, s_slots, s_load[2];
+    __shared__ int s_max, s_slots, s_load[2], s_join;
     const int tid = threadIdx.x;
     const int tok = kBwd ? 128 : 2 * p.TT;  // tokens per block
     int* pre = p.S <= kPlanSmemSeqs ? s_prefix : p.prefix;
@@ -106,6 +106,7 @@ __device__ void build_plan(const PlanParams& p) {
         s_max = 1;
         s_slots = 0;
         s_load[0] = s_load[1] = 0;
+        s_join = kPlanJoinFew;
     }
     int carry = 0, bad = 0, q_carry = 0;
     for (int base = 0; base < p.S; base += kPlanThreads) {
@@ -254,6 +255,7 @@ __device__ void build_plan(const PlanParams& p) {
         for (int b = tid; b < n_blocks; b += kPlanThreads) {
             const Block x = get(b);
             const int parts = with_parts ? plan_parts(x.cost, limit) : 1, q = x.tiles / parts, r = x.tiles % parts;
+            if (parts > 1 && 4 * x.n > p.TT) s_join = kPlanJoinTiles;  // more than 32 rows
             if (r > 0) atomicAdd(&s_hist[bucket(x, q + 1)], r);
             atomicAdd(&s_hist[bucket(x, q)], parts - r);
         }
@@ -273,7 +275,7 @@ __device__ void build_plan(const PlanParams& p) {
     if (longest > limit) {
         sort_items(true);
         cut = true;
-        const int with = s_load[1] + kPlanJoinTiles;
+        const int with = s_load[1] + s_join;
         const int start = s_hist[tid], items_cut = n_items;
         sort_items(false);
         if (with < s_load[0]) {
