@@ -614,3 +614,120 @@ def test_timeout_is_reported_and_the_context_survives(cuda_api, which):
             packed_ref.check(name, x, ref)
     else:
         packed_ref.check("o", got[0], ref)
+
+
+# ------------------------------------------------------------------ calls that are allowed and easy to forget
+def test_gradients_into_one_fused_tensor(cuda_api):
+    """dq, dk, dv as views of the gradient of a fused projection's output, whose other columns stay."""
+    for Hq, Hkv, D in ((8, 2, 128), (6, 2, 64)):
+        q, k, v, dout, starts, cu = _batch([70, 200, 1], Hq, Hkv, D, 101, before=2, after=3, fused=True)
+        o, lse = cuda_api.attn_packed_fwd(q, k, v, cu, causal=True)
+        g = torch.full((q.shape[0], Hq + 2 * Hkv + 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        cuda_api.attn_packed_bwd(q, k, v, o, lse, dout, cu, causal=True, dq=g[:, :Hq], dk=g[:, Hq:Hq + Hkv],
+                                 dv=g[:, Hq + Hkv:Hq + 2 * Hkv])
+        ref = packed_ref.packed(q, k, v, starts, True, 0, dout=dout)
+        for name, x in (("dq", g[:, :Hq]), ("dk", g[:, Hq:Hq + Hkv]), ("dv", g[:, Hq + Hkv:Hq + 2 * Hkv])):
+            packed_ref.check(name, x, ref)
+        assert bool((g[:, -1] == 7).all()) and bool((g[:2] == 7).all()) and bool((g[-3:] == 7).all())
+
+
+def test_chunk_shared_pages(cuda_api):
+    """Two sequences share the pages of a common beginning (one of them a page in two places of its row)."""
+    kp, vp, table = _cache([64, 64], 2, 128, 102, spare=6, extra_blocks=6)
+    shared = table[0, :4].clone()
+    rows = torch.full((2, 8), -1, dtype=torch.int32)
+    free = [p for p in range(kp.shape[0]) if p not in shared.tolist()]
+    rows[0, :6] = torch.tensor(shared.tolist() + free[:2])
+    rows[1, :7] = torch.tensor(shared.tolist() + [int(shared[1])] + free[2:4])
+    new, total = [20, 30], [64 + 20, 80 + 30]
+    q, kn, vn, _, starts, cu = _batch(new, 8, 2, 128, 103)
+    o, lse = cuda_api.attn_chunk_paged(q, kp, vp, rows.cuda(), torch.tensor(total, dtype=torch.int32, device="cuda"), cu,
+                                       k_new=kn, v_new=vn)
+    assert cuda_api.device_status() == 0
+    for s in range(2):
+        a, b = starts[s], starts[s + 1]
+        k_all, v_all = _rows(kp, rows, s, total[s]), _rows(vp, rows, s, total[s])
+        assert torch.equal(k_all[-new[s]:], kn[a:b]) and torch.equal(v_all[-new[s]:], vn[a:b])
+        ref = packed_ref.attend(q[a:b], k_all, v_all, True, 0)
+        packed_ref.check("o", o[a:b], ref)
+        packed_ref.check("lse", lse[a:b].t(), ref)
+
+
+def test_chunk_many_sequences(cuda_api):
+    """More sequences than the plan keeps in shared memory, one or no token each."""
+    rng = random.Random(104)
+    new = [rng.choice([0, 1, 1, 2]) for _ in range(2300)]
+    ctx = [rng.choice([0, 3, 15, 16, 40]) for _ in new]
+    ctx = [c if n or c else 1 for c, n in zip(ctx, new)]
+    _check_chunk(cuda_api, ctx, new, 4, 2, 64, 0, seed=105)
+
+
+def test_rows_beyond_32_bit_offsets(cuda_api):
+    """A sequence at the end of tensors of more than 2^31 elements (and bytes of a gradient, a workspace)."""
+    T, Hq, Hkv, D, n = 540_000, 32, 8, 128, 300
+    g = _gen(106)
+    q, dout = (torch.empty(T, Hq, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.empty(T, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for x in (q, dout, k, v):
+        x[T - n - 200:] = NAN
+        x[T - n:] = _randn(g, n, *x.shape[1:])
+    cu = torch.tensor([T - n, T], dtype=torch.int32, device="cuda")
+    ref = packed_ref.attend(q[T - n:], k[T - n:], v[T - n:], True, 0, dout=dout[T - n:])
+    o, lse = cuda_api.attn_packed_fwd(q, k, v, cu, causal=True)
+    packed_ref.check("o", o[T - n:], ref)
+    packed_ref.check("lse", lse[:, T - n:], ref)
+    for name, x in zip(("dq", "dk", "dv"), cuda_api.attn_packed_bwd(q, k, v, o, lse, dout, cu, causal=True)):
+        packed_ref.check(name, x[T - n:], ref)
+    pos = torch.zeros(1, T, dtype=torch.int32, device="cuda")
+    pos[0, T - n:] = torch.arange(n, dtype=torch.int32, device="cuda")
+    first = q[T - n:].clone()
+    y, _ = cuda_api.attn_rope_axes(q, k, pos, [64], q_out=q, k_out=k)
+    want, tol = packed_ref.rope_axes(first, pos[:, T - n:], [64], False, False, False, 1e4)
+    assert bool(((y[T - n:].double() - want).abs() <= tol).all())
+    assert cuda_api.device_status() == 0
+
+
+def test_pages_beyond_32_bit_offsets(cuda_api):
+    """Pages at the end of pools of more than 2^31 elements."""
+    pool, Hkv, D, n, ctx = 140_000, 8, 128, 40, 500
+    kp, vp = (torch.empty(pool, Hkv, 16, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pages = (ctx + n + 15) // 16
+    table = torch.arange(pool - pages, pool, dtype=torch.int32).flip(0)[None].contiguous()
+    g = _gen(107)
+    for x in (kp, vp):
+        x[pool - pages:] = _randn(g, pages, Hkv, 16, D)
+    q, kn, vn, _, _, cu = _batch([n], 16, Hkv, D, 108)
+    o, lse = cuda_api.attn_chunk_paged(q, kp, vp, table.cuda(), torch.tensor([ctx + n], dtype=torch.int32, device="cuda"),
+                                       cu, k_new=kn, v_new=vn)
+    assert cuda_api.device_status() == 0
+    k_all, v_all = _rows(kp, table, 0, ctx + n), _rows(vp, table, 0, ctx + n)
+    assert torch.equal(k_all[ctx:], kn) and torch.equal(v_all[ctx:], vn)
+    packed_ref.check("o", o, packed_ref.attend(q, k_all, v_all, True, 0))
+
+
+def test_backward_and_chunks_on_two_streams(cuda_api):
+    """A training step and a serving step at once, on streams of their own, equal the calls alone."""
+    q, k, v, dout, starts, cu = _batch([400, 90], 8, 2, 64, 109)
+    kp, vp, table = _cache([900, 300], 2, 64, 110)
+    new = [50, 1]
+    qc, kn, vn, _, _, cuc = _batch(new, 8, 2, 64, 111)
+    lens, table_d = torch.tensor([900, 300], dtype=torch.int32, device="cuda"), table.cuda()
+    chunk = lambda s: cuda_api.attn_chunk_paged(qc, kp, vp, table_d, lens, cuc, k_new=kn, v_new=vn, stream=s)
+
+    def train(s):
+        o, lse = cuda_api.attn_packed_fwd(q, k, v, cu, causal=True, stream=s)
+        return (o, lse) + tuple(cuda_api.attn_packed_bwd(q, k, v, o, lse, dout, cu, causal=True, stream=s))
+
+    alone = train(None), chunk(None)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    ref = packed_ref.packed(q, k, v, starts, True, 0, dout=dout)
+    for _ in range(4):
+        for s in (s1, s2):
+            s.wait_stream(torch.cuda.current_stream())
+        a, b = train(s1), chunk(s2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(b, alone[1]))
+        for name, x, y in zip(("o", "lse", "dq", "dk", "dv"), a, alone[0]):
+            packed_ref.check(name, x, ref)
+            assert name == "dq" or torch.equal(x, y)  # (dq's order of summation is free)
