@@ -309,7 +309,8 @@ __device__ __forceinline__ uint32_t dq_box(int cg, int qw, const uint8_t* sQ, co
 // kPacked: the CTA's key tile is the (block number / Hkv)-th of the plan's order, of a sequence of N
 // tokens whose rows start at row0 of the packed tensors; a step is one query tile of TT tokens times the G
 // heads (the unpacked kernel walks 128 tokens of one head after the other: at four heads to a K/V head the
-// ends of 16 documents of 705 tokens on average then leave 8% more rows empty). Rows behind the sequence's
+// ends of 16 documents of 705 tokens on average then leave 8% more rows empty, and the whole training step
+// took 769 us instead of 730). Rows behind the sequence's
 // end belong to another sequence or to nobody and may hold NaN: such queries and keys get P = dS = 0 by
 // selection, and where they are summed over (dV and dK over queries, dQ over keys) the product stops at the
 // last 16-row slice with a valid row, whose other rows are set to zero in shared memory by the elementwise

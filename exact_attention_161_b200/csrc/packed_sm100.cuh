@@ -19,15 +19,33 @@
 //     copy of the queries: steps alternate between the first and the second half of the item's key tiles,
 //     and the first warpgroup joins both states out of Tensor Memory at the end. A tile of one warpgroup
 //     alone takes as long as a tile of both, so this halves the time of single tokens and short chunks.
-//   Pages. A 128-key tile of the cache is eight 16-token pages, each fetched by its own box; lane i
-//     of the producer warp looks up and issues page i.
+//   Pages. A 128-key tile of the cache is eight 16-token pages, each fetched by its own boxes; lane i
+//     of a producer warp looks up and issues page i. K and V have a producer warp each.
 //   Tails. A sequence ends inside a key tile; the rows behind its end belong to another sequence or
 //     to nobody and may hold NaN. Scores are masked by selection. For P V, 0 * NaN would survive, so
 //     the product stops at the last 16-key slice with a visible key (one MMA per slice), and the
 //     rest of that slice's V rows are set to zero in shared memory by the softmax warps before P is
 //     handed over.
 //
-// The roles, TMEM layout, issue order and softmax arithmetic are those of attn_fwd_kernel.
+// Roles: warps 0-3 and 4-7 softmax, 8 producer of Q, K and the work ring, 9 MMA issuer, then at D = 64 an
+// issuer of the output products, then the producer of V. TMEM layout, issue order (D = 128) and softmax
+// arithmetic are those of attn_fwd_kernel, but P is handed over in two halves, so that the product with the
+// first runs while the second is computed (three long documents 2,243 -> 2,182 us; three quarters and one
+// quarter measured the same at D = 128 and 10% slower at D = 64). The eighth of the exponentials on the FMA
+// pipe uses a polynomial of degree 4 and not 3: over a window of a few keys the sum of the probabilities
+// carries its whole error (1.0e-4 relative, against 2.9e-6).
+//
+// What bounds it (B200, measured with clock64 in a copy of the kernel):
+//   D = 128, long sequences: the chain of one query tile from its scores through the softmax (1,900 clocks)
+//     and its 16 products back to the next scores (1,500 to 1,650); two tiles share 2,048 clocks of tensor work
+//     in a step of 3,300 to 3,500. Three documents of 4,000 to 12,000 tokens, 32 heads on 8: 2.68 TFLOP in
+//     2,160 to 2,190 us, 1,230 TFLOP/s, 0.75 of the measured bf16 rate (attn_fwd_kernel 1,237 on one
+//     sequence of 8,192).
+//   Short sequences: 4,200 to 5,500 clocks an item outside its steps (the last tile's masks, the last
+//     product, O to memory, the first scores): 24 prompts of 100 to 1,500 tokens 141 us, of which O's stores
+//     cost 8 and the masks 4 (left out in copies).
+//   D = 64: the exponentials (SFU 60% busy); 12 images of 200 to 3,300 patches 200 us, 590 TFLOP/s.
+//   Single tokens: reading the keys, 64 on 16,000 tokens each 5.7 TB/s (0.87 of the copy rate).
 #pragma once
 #include "common.cuh"
 #include "fwd_sm100.cuh"
@@ -138,7 +156,7 @@ __device__ void build_plan(const PlanParams& p) {
     if (bad) {
         if (tid == 0) {
             raise_status(kStatusBadOffsets);
-            PlanHeader h{0, 0, 1, 0};
+            PlanHeader h{0, 0, {0, 0}};
             *p.header = h;
         }
         return;
@@ -194,7 +212,7 @@ __device__ void build_plan(const PlanParams& p) {
             p.order[p.start[s] + t.t] = b;
         }
         if (tid == 0) {
-            PlanHeader h{n_blocks, 0, 0, 0};
+            PlanHeader h{n_blocks, 0, {0, 0}};
             *p.header = h;
         }
         return;
@@ -317,7 +335,7 @@ __device__ void build_plan(const PlanParams& p) {
     }
     __syncthreads();
     if (tid == 0) {
-        PlanHeader h{n_items, s_slots, 0, 0};
+        PlanHeader h{n_items, 0, {0, 0}};
         *p.header = h;
     }
 }

@@ -68,10 +68,9 @@ struct PackedTile {
 
 // Head of a plan in the workspace.
 struct PlanHeader {
-    int n_items;   // forward items (each for every K/V head); backward tiles
-    int n_slots;   // partial-state slots in use
-    int bad;       // the offsets are invalid: there are no items
+    int n_items;   // forward items (each for every K/V head); backward key tiles; 0 with invalid offsets
     int taken;     // items taken beyond the first of every CTA
+    int pad[2];
 };
 
 // Key tiles visible to tokens [first, last] (positions) of a sequence of kv_len keys: [jb, jb + n).
