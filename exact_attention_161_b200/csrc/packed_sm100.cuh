@@ -31,18 +31,19 @@
 // issuer of the output products, then the producer of V. TMEM layout, issue order (D = 128) and softmax
 // arithmetic are those of attn_fwd_kernel, but P is handed over in two halves, so that the product with the
 // first runs while the second is computed (three long documents 2,243 -> 2,182 us; three quarters and one
-// quarter measured the same at D = 128 and 10% slower at D = 64). The eighth of the exponentials on the FMA
-// pipe uses a polynomial of degree 4 and not 3: over a window of a few keys the sum of the probabilities
-// carries its whole error (1.0e-4 relative, against 2.9e-6).
+// quarter measured the same at D = 128 and 10% slower at D = 64). All exponentials are the
+// SFU's: an eighth or a sixteenth of them on the FMA pipe, as attn_fwd_kernel has it, measured the same or
+// up to 5% slower here (with a polynomial of degree 4, as the sum of a few probabilities would show the
+// error of one of degree 3), a quarter 10 to 18%.
 //
 // What bounds it (B200, measured with clock64 in a copy of the kernel):
 //   D = 128, long sequences: the chain of one query tile from its scores through the softmax (1,900 clocks)
 //     and its 16 products back to the next scores (1,500 to 1,650); two tiles share 2,048 clocks of tensor work
 //     in a step of 3,300 to 3,500. Three documents of 4,000 to 12,000 tokens, 32 heads on 8: 2.68 TFLOP in
-//     2,160 to 2,190 us, 1,230 TFLOP/s, 0.75 of the measured bf16 rate (attn_fwd_kernel 1,237 on one
+//     2,130 to 2,190 us, 1,220 to 1,260 TFLOP/s, 0.75 of the measured bf16 rate (attn_fwd_kernel 1,237 on one
 //     sequence of 8,192).
 //   Short sequences: 4,200 to 5,500 clocks an item outside its steps (the last tile's masks, the last
-//     product, O to memory, the first scores): 24 prompts of 100 to 1,500 tokens 141 us, of which O's stores
+//     product, O to memory, the first scores): 24 prompts of 100 to 1,500 tokens 137 to 141 us, of which O's stores
 //     cost 8 and the masks 4 (left out in copies).
 //   D = 64: the exponentials (SFU 60% busy); 12 images of 200 to 3,300 patches 200 us, 590 TFLOP/s.
 //   Single tokens: reading the keys, 64 on 16,000 tokens each 5.7 TB/s (0.87 of the copy rate).
@@ -1080,11 +1081,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                         x0 = make_float2(ptx::ex2(x0.x), ptx::ex2(x0.y));
                         x1 = make_float2(ptx::ex2(x1.x), ptx::ex2(x1.y));
                         x2 = make_float2(ptx::ex2(x2.x), ptx::ex2(x2.y));
-                        // 1/8 of the exponentials on the FMA pipe, as in attn_fwd_kernel
-                        if ((k / 8) % 2 == 0)
-                            x3 = make_float2(ptx::ex2_poly4(x3.x), ptx::ex2_poly4(x3.y));
-                        else
-                            x3 = make_float2(ptx::ex2(x3.x), ptx::ex2(x3.y));
+                        x3 = make_float2(ptx::ex2(x3.x), ptx::ex2(x3.y));
                         acc0 = ptx::fadd2(acc0, x0);
                         acc1 = ptx::fadd2(acc1, x1);
                         acc2 = ptx::fadd2(acc2, x2);
@@ -1176,8 +1173,9 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 ptx::mbar_arrive(&bar->o_empty[wg]);
                 if (two_sided) ptx::mbar_arrive(&bar->o_empty[1]);
             };
+            // (loops kept rolled: what runs once an item competes for instruction cache; 24 prompts 139 -> 137 us)
             if (x.parts > 1) {
-#pragma unroll
+#pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t v[32];
                     load_output(cc * 32, v);
@@ -1199,7 +1197,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 const int h = x.g * p.G + my_head;
                 uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row * p.Hq + h) * D);
                 const bool sectors = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;  // whole 32-byte sectors
-#pragma unroll
+#pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t v[32], w[16];
                     load_output(cc * 32, v);

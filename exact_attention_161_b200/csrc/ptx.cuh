@@ -489,19 +489,6 @@ __device__ __forceinline__ float2 ex2_poly2(float2 x) {
                        __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
 }
 
-// As ex2_poly with a degree-4 polynomial from the same fit: largest relative error 2.9e-06, where the
-// sum of the probabilities has to keep more than bf16's bits (logsumexp over few keys).
-__device__ __forceinline__ float ex2_poly4(float x) {
-    x = fmaxf(x, -127.f);
-    const float t = x + 12582912.f;  // as in ex2_poly
-    const float f = x - (t - 12582912.f);
-    float q = fmaf(0x1.3a02a8p-7f, f, 0x1.c9fc4p-5f);
-    q = fmaf(q, f, 0x1.ec0378p-3f);
-    q = fmaf(q, f, 0x1.62e12cp-1f);
-    q = fmaf(q, f, 1.f);
-    return __int_as_float(__float_as_int(q) + (__float_as_int(t) << 23));
-}
-
 // max(a, b, c) in one instruction (sm_100a).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;
