@@ -306,15 +306,16 @@ __device__ __forceinline__ uint32_t dq_box(int cg, int qw, const uint8_t* sQ, co
 // steps back until the TMA has read it (about 64 KB at ~20 bytes per clock per SM under load), so
 // issuing it earlier in the step gains nothing.
 //
-// kPacked: the CTA's key tile is the (block number / Hkv)-th of the plan's order, of a sequence of N
-// tokens whose rows start at row0 of the packed tensors; a step is one query tile of TT tokens times the G
-// heads (the unpacked kernel walks 128 tokens of one head after the other: at four heads to a K/V head the
-// ends of 16 documents of 705 tokens on average then leave 8% more rows empty, and the whole training step
-// took 769 us instead of 730). Rows behind the sequence's
-// end belong to another sequence or to nobody and may hold NaN: such queries and keys get P = dS = 0 by
-// selection, and where they are summed over (dV and dK over queries, dQ over keys) the product stops at the
-// last 16-row slice with a valid row, whose other rows are set to zero in shared memory by the elementwise
-// warps before P^T (dO) and dS^T (Q, K) are handed over.
+// kPacked: the CTA's key tile is the (block number / Hkv)-th of the plan's order, of a sequence of N tokens
+// whose rows start at row0 of the packed tensors; a step is one query tile of TT tokens times the G heads
+// (walking 128 tokens of one head after the other, as the unpacked kernel does, left 8% more rows empty at
+// the ends of 16 documents of 705 tokens on average, and the whole training step took 769 us instead of
+// 730). Rows behind the sequence's end belong to another sequence or to nobody and may hold NaN: such
+// queries and keys get P = dS = 0 by selection, and where they are summed over (dV and dK over queries, dQ
+// over keys) the product stops at the last 16-row slice with a valid row, whose other rows are set to zero
+// in shared memory by the elementwise warps before P^T (dO) and dS^T (Q, K) are handed over.
+// What bounds it is the chain of a step, as in the unpacked kernel: 440 us for those documents, the tensor
+// pipe 38% busy, 660 TFLOP/s of their visible pairs (1.25 times as many are computed).
 template <int D, bool kPacked = false>
 __global__ void __launch_bounds__(BwdCfg<D>::THREADS, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

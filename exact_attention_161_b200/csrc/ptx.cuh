@@ -208,48 +208,6 @@ __device__ __forceinline__ void mma_ts_if(uint32_t issue, uint32_t d_tmem, uint3
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
         : "memory");
 }
-// A whole score tile S = Q K^T of 128 x 128 x D (a new sum), and a whole output tile O += P V of
-// 128 x D x 128 (P in TMEM, V MN-major), as one block each: operands are stepped by constants.
-template <int D>
-__device__ __forceinline__ void mma_ss_tile(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
-    if constexpr (D == 128)
-        asm volatile(
-            "{\n\t.reg .pred q, t, f;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\tsetp.ne.b32 f, 0, 0;\n\t"
-            "add.s64 x, %1, 0;\n\tadd.s64 y, %2, 0;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, f;\n\t"
-            "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-            "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-            "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-            "add.s64 x, %1, 1024;\n\tadd.s64 y, %2, 1024;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-            "add.s64 x, %1, 1026;\n\tadd.s64 y, %2, 1026;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-            "add.s64 x, %1, 1028;\n\tadd.s64 y, %2, 1028;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-            "add.s64 x, %1, 1030;\n\tadd.s64 y, %2, 1030;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-            "}" ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(issue)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred q, t, f;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\tsetp.ne.b32 f, 0, 0;\n\t"
-            "add.s64 x, %1, 0;\n\tadd.s64 y, %2, 0;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, f;\n\t"
-            "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-            "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-            "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-            "}" ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(issue)
-            : "memory");
-}
-template <int D>
-__device__ __forceinline__ void mma_ts_tile(uint32_t issue, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
-    asm volatile(
-        "{\n\t.reg .pred q, t;\n\t.reg .b32 z;\n\t.reg .b64 y;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-        "add.s32 z, %1, 0;\n\tadd.s64 y, %2, 0;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [z], y, %3, t;\n\t"
-        "add.s32 z, %1, 8;\n\tadd.s64 y, %2, 128;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [z], y, %3, t;\n\t"
-        "add.s32 z, %1, 16;\n\tadd.s64 y, %2, 256;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [z], y, %3, t;\n\t"
-        "add.s32 z, %1, 24;\n\tadd.s64 y, %2, 384;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [z], y, %3, t;\n\t"
-        "add.s32 z, %1, 32;\n\tadd.s64 y, %2, 512;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [z], y, %3, t;\n\t"
-        "add.s32 z, %1, 40;\n\tadd.s64 y, %2, 640;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [z], y, %3, t;\n\t"
-        "add.s32 z, %1, 48;\n\tadd.s64 y, %2, 768;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [z], y, %3, t;\n\t"
-        "add.s32 z, %1, 56;\n\tadd.s64 y, %2, 896;\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], [z], y, %3, t;\n\t"
-        "}" ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(issue)
-        : "memory");
-}
 // The FP8 forms (kind::f8f6f4: e4m3 A and B, K = 32 per instruction, fp32 accumulation; A from
 // TMEM packs four e4m3 per 32-bit column), predicated the same way.
 __device__ __forceinline__ void mma_ss_f8_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
