@@ -1175,14 +1175,20 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
             };
             // (loops kept rolled: what runs once an item competes for instruction cache; 24 prompts 139 -> 137 us)
             if (x.parts > 1) {
+                // rows lie at multiples of 256 bytes from the workspace's base, which may be 16 modulo 32
+                const bool sectors = (reinterpret_cast<uintptr_t>(p.ws_o) & 31) == 0;
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t v[32];
                     load_output(cc * 32, v);
-                    if (live) {
-                        uint32_t* dst = reinterpret_cast<uint32_t*>(p.ws_o + prow * D + cc * 32);  // 256-byte aligned rows
+                    uint32_t* dst = reinterpret_cast<uint32_t*>(p.ws_o + prow * D + cc * 32);
+                    if (live && sectors) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 8) ptx::st_global_v8(dst + k, v + k);
+                    } else if (live) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<uint4*>(dst + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
                     }
                 }
                 output_read();

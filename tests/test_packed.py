@@ -731,3 +731,62 @@ def test_backward_and_chunks_on_two_streams(cuda_api):
         for name, x, y in zip(("o", "lse", "dq", "dk", "dv"), a, alone[0]):
             packed_ref.check(name, x, ref)
             assert name == "dq" or torch.equal(x, y)  # (dq's order of summation is free)
+
+
+# ------------------------------------------------------------------ alignment, values that are not finite, the work list
+def _plan_items(ws, S):
+    """The forward work list in a workspace: int32 [items, 8] (first query row, position, sequence or first key
+    row, keys, first key tile, key tiles, tokens | part << 10 | (parts - 1) << 20, slot)."""
+    w = ws.cpu()
+    n = int(w[:4].view(torch.int32))
+    at = 256 + ((S + 1) * 4 + 255) // 256 * 256
+    return w[at:at + 32 * n].clone().view(torch.int32).view(n, 8)
+
+
+def _at_16_modulo_32(shape, dtype, fill):
+    """A tensor whose memory starts 16 bytes behind a 32-byte border."""
+    n = 1
+    for x in shape:
+        n *= x
+    raw = torch.empty(n + 64, dtype=dtype, device="cuda")
+    size = raw.element_size()
+    at = ((16 - raw.data_ptr()) % 32) // size
+    x = raw[at:at + n].view(shape)
+    assert x.data_ptr() % 32 == 16
+    return x.fill_(fill)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 1, 128), (4, 4, 64), (6, 2, 64)])
+def test_buffers_at_16_byte_borders(cuda_api, Hq, Hkv, D):
+    """Workspace and outputs 16 bytes behind a 32-byte border: what the header asks for and no more, on calls
+    that cut keys into parts (blocks of two query tiles, single tokens) and on one that cuts nothing."""
+    ws = lambda n: _at_16_modulo_32((n,), torch.uint8, 0xff)
+    out = lambda T: _at_16_modulo_32((T, Hq, D), torch.bfloat16, 7.0)
+    for lens, cut in (([2500, 1, 3000], True), ([40, 130], False)):
+        T, S = sum(lens), len(lens)
+        q, k, v, dout, starts, cu = _batch(lens, Hq, Hkv, D, 120)
+        w = ws(cuda_api.packed_fwd_workspace_size(T, S, Hq, Hkv, D))
+        o, lse = cuda_api.attn_packed_fwd(q, k, v, cu, causal=True, o=out(T), workspace=w)
+        assert bool(((_plan_items(w, S)[:, 6] >> 20) > 0).any()) == cut
+        ref = packed_ref.packed(q, k, v, starts, True, 0, dout=dout)
+        packed_ref.check("o", o, ref)
+        packed_ref.check("lse", lse, ref)
+        w = ws(cuda_api.packed_bwd_workspace_size(T, S, Hq, Hkv, D))
+        grads = [_at_16_modulo_32(x.shape, torch.bfloat16, 7.0) for x in (q, k, v)]
+        cuda_api.attn_packed_bwd(q, k, v, o, lse, dout, cu, causal=True, dq=grads[0], dk=grads[1], dv=grads[2],
+                                 workspace=w)
+        for name, x in zip(("dq", "dk", "dv"), grads):
+            packed_ref.check(name, x, ref)
+    for new, total in (([1, 1], [9000, 700]), ([300, 2], [6000, 40])):
+        kp, vp, table = _cache(total, Hkv, D, 121)
+        q, kn, vn, _, starts, cu = _batch(new, Hq, Hkv, D, 122)
+        w = ws(cuda_api.chunk_workspace_size(sum(new), 2, table.shape[1], 16, Hq, Hkv, D))
+        o, lse = cuda_api.attn_chunk_paged(q, kp, vp, table.cuda(), torch.tensor(total, dtype=torch.int32, device="cuda"),
+                                           cu, k_new=kn, v_new=vn, o=out(sum(new)), workspace=w)
+        assert bool(((_plan_items(w, 2)[:, 6] >> 20) > 0).any())
+        for s in range(2):
+            a, b = starts[s], starts[s + 1]
+            ref = packed_ref.attend(q[a:b], _rows(kp, table, s, total[s]), _rows(vp, table, s, total[s]), True, 0)
+            packed_ref.check("o", o[a:b], ref)
+            packed_ref.check("lse", lse[a:b].t(), ref)
+    assert cuda_api.device_status() == 0
