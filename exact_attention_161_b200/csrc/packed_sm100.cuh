@@ -503,6 +503,8 @@ __device__ __forceinline__ void mask_columns(float (&s)[N], int lo, int hi) {
 // L = sum 2^(m_i - M) l_i, O = sum 2^(m_i - M) o_i / L, LSE = (M + log2 L) ln 2, in ascending order of i.
 // The statistics go a row to a lane, the outputs a row to the warp, four rows and parts at a time: what
 // counts is how many loads are in flight.
+// A row that sees a NaN or a score of +inf has a sum of NaN in that part (beside a maximum of -inf or +inf)
+// and comes out as NaN, as from a block that was not cut.
 template <int D>
 __device__ __noinline__ void join_parts(const PackedParams& p, int g, int q_row, int tok, int slot, int parts, int wg, int quad) {
     constexpr int PER = D / 32;  // columns of a lane
@@ -531,14 +533,14 @@ __device__ __noinline__ void join_parts(const PackedParams& p, int g, int q_row,
         L *= M == -INFINITY ? 0.f : ptx::ex2(M - top);
         M = top;
 #pragma unroll
-        for (int j = 0; j < B; ++j)  // -inf: none of the row's keys, and no output
-            if (base + j < parts && x[j].x != -INFINITY) L = fmaf(ptx::ex2(x[j].x - M), x[j].y, L);
+        for (int j = 0; j < B; ++j)  // a sum of 0: none of the row's keys, and no output
+            if (base + j < parts && x[j].y != 0.f) L = fmaf(ptx::ex2(x[j].x - M), x[j].y, L);
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = 1.f / L;  // (NaN of any part stays, whatever weight the part has)
     if (lane < rows && p.lse != nullptr) {
         const int r = quad * 32 + lane, t = r / p.G, h = g * p.G + r - t * p.G;
         const size_t row = static_cast<size_t>(q_row) + t;
-        p.lse[row * p.lse_t + h * p.lse_h] = L > 0.f ? (M + ptx::lg2(L)) * kLn2 : -INFINITY;
+        p.lse[row * p.lse_t + h * p.lse_h] = (M + ptx::lg2(L)) * kLn2;
     }
     constexpr int R = 4, P = 4;  // rows and parts at a time
     for (int r0 = 0; r0 < rows; r0 += R) {
@@ -1198,7 +1200,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                 }
                 join_parts<D>(p, x.g, x.q_row + q_tile * p.TT, tok, x.slot, x.parts, wg, warp & 3);
             } else {
-                const float inv_l = l > 0.f ? 1.f / l : 0.f;
+                const float inv_l = 1.f / l;
                 const size_t row = static_cast<size_t>(x.q_row + q_tile * p.TT + my_tok);
                 const int h = x.g * p.G + my_head;
                 uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (row * p.Hq + h) * D);
@@ -1222,7 +1224,7 @@ __global__ void __launch_bounds__(PackedCfg<D>::THREADS, 1)
                     }
                 }
                 if (live && p.lse != nullptr)
-                    p.lse[row * p.lse_t + h * p.lse_h] = l > 0.f ? (m_used + ptx::lg2(l)) * kLn2 : -INFINITY;
+                    p.lse[row * p.lse_t + h * p.lse_h] = (m_used + ptx::lg2(l)) * kLn2;
             }
             par ^= kItems;
             release_work();

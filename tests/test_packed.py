@@ -790,3 +790,51 @@ def test_buffers_at_16_byte_borders(cuda_api, Hq, Hkv, D):
             packed_ref.check("o", o[a:b], ref)
             packed_ref.check("lse", lse[a:b].t(), ref)
     assert cuda_api.device_status() == 0
+
+
+def _spoil(q, k, row):
+    """Queries that are not finite: rows `row` to `row` + 3 of head 0 get a NaN, an infinity (scores of both
+    signs), and an infinity of the sign that makes every score -inf (k[:, 0, 9] is positive)."""
+    k[:, 0, 9] = k[:, 0, 9].abs() + 0.125
+    q[row, 0, 3], q[row + 1, 0, 5], q[row + 2, 0, 7], q[row + 3, 0, 9] = NAN, float("inf"), -float("inf"), -float("inf")
+
+
+def _check_spoiled(ref, o, lse, row, n):
+    """o [n, Hq, D], lse [Hq, n] of one sequence: NaN in head 0 of the four rows (lse -inf where all scores
+    are), everything else as the plain form says."""
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[row:row + 4] = True
+    assert bool(torch.isnan(ref["o"][bad, 0]).all()) and bool(torch.isnan(o[bad, 0].float()).all())
+    assert bool(torch.isnan(lse[0, row:row + 3]).all()) and lse[0, row + 3].item() == -float("inf")
+    ref["lse"][0, bad] = NAN  # (compared above)
+    packed_ref.check("o", o, ref)
+    packed_ref.check("lse", lse, ref)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 1, 128), (4, 4, 64), (6, 2, 64)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 700), (False, 0)])
+def test_queries_that_are_not_finite(cuda_api, Hq, Hkv, D, causal, window):
+    """A NaN or infinite query shows in its own row, whether its block's keys are cut into parts or not, and
+    in every part."""
+    for lens, row in (([2500, 3000], 5), ([2500, 3000], 2990), ([130, 90], 60)):
+        q, k, v, _, starts, cu = _batch(lens, Hq, Hkv, D, 130)
+        a = starts[1]
+        _spoil(q[a:], k[a:], row)
+        o, lse = cuda_api.attn_packed_fwd(q, k, v, cu, causal=causal, window=window)
+        packed_ref.check("o", o[:a], packed_ref.attend(q[:a], k[:a], v[:a], causal, window))
+        _check_spoiled(packed_ref.attend(q[a:], k[a:], v[a:], causal, window), o[a:], lse[:, a:], row, lens[1])
+    assert cuda_api.device_status() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (4, 4, 64)])
+@pytest.mark.parametrize("new,total", [([4], [9000]), ([400], [7000]), ([4], [60])])
+def test_chunk_queries_that_are_not_finite(cuda_api, Hq, Hkv, D, new, total):
+    kp, vp, table = _cache(total, Hkv, D, 131)
+    q, kn, vn, _, _, cu = _batch(new, Hq, Hkv, D, 132)
+    _spoil(q, kn, new[0] - 4)
+    kp[:, 0, :, 9] = kp[:, 0, :, 9].abs() + 0.125
+    o, lse = cuda_api.attn_chunk_paged(q, kp, vp, table.cuda(), torch.tensor(total, dtype=torch.int32, device="cuda"),
+                                       cu, k_new=kn, v_new=vn)
+    ref = packed_ref.attend(q, _rows(kp, table, 0, total[0]), _rows(vp, table, 0, total[0]), True, 0)
+    _check_spoiled(ref, o, lse.t(), new[0] - 4, new[0])
+    assert cuda_api.device_status() == 0
