@@ -516,6 +516,7 @@ __device__ __noinline__ void join_parts(const PackedParams& p, int g, int q_row,
     if (lane == 0)
         last = ptx::atomic_add_acq_rel(p.count + (static_cast<size_t>(slot) * p.Hkv + g) * kPlanWarps + wg * 4 + quad, 1) == parts - 1;
     if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    __syncwarp();  // lane 0 has acquired the other parts' states: the shuffle alone orders no memory
     const size_t step = static_cast<size_t>(p.Hkv) * 256;  // rows from one part's state to the next
     const int rows = min(32, tok * p.G - quad * 32);  // live rows of this warp
     const size_t row0 = (static_cast<size_t>(slot) * p.Hkv + g) * 256 + wg * 128 + quad * 32;

@@ -838,3 +838,28 @@ def test_chunk_queries_that_are_not_finite(cuda_api, Hq, Hkv, D, new, total):
     ref = packed_ref.attend(q, _rows(kp, table, 0, total[0]), _rows(vp, table, 0, total[0]), True, 0)
     _check_spoiled(ref, o, lse.t(), new[0] - 4, new[0])
     assert cuda_api.device_status() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (6, 2, 64)])
+def test_joined_parts_repeat_bit_for_bit(cuda_api, Hq, Hkv, D):
+    """Single tokens and chunks whose keys are cut into many parts, joined by whichever warp is last, each time
+    on a workspace that holds other calls' states."""
+    new, total = [1, 40, 1, 3], [20000, 9000, 300, 16]
+    kp, vp, table = _cache(total, Hkv, D, 133)
+    q, kn, vn, _, starts, cu = _batch(new, Hq, Hkv, D, 134)
+    lens, t = torch.tensor(total, dtype=torch.int32, device="cuda"), table.cuda()
+    w = torch.empty(cuda_api.chunk_workspace_size(sum(new), 4, table.shape[1], 16, Hq, Hkv, D), dtype=torch.uint8,
+                    device="cuda")
+    first = cuda_api.attn_chunk_paged(q, kp, vp, t, lens, cu, k_new=kn, v_new=vn, workspace=w)
+    assert int(_plan_items(w, 4)[:, 6].max() >> 20) >= 16  # parts - 1 of the longest
+    for s in range(4):
+        a, b = starts[s], starts[s + 1]
+        ref = packed_ref.attend(q[a:b], _rows(kp, table, s, total[s]), _rows(vp, table, s, total[s]), True, 0)
+        packed_ref.check("o", first[0][a:b], ref)
+        packed_ref.check("lse", first[1][a:b].t(), ref)
+    other = q.flip(0).contiguous()
+    for _ in range(30):
+        cuda_api.attn_chunk_paged(other, kp, vp, t, lens, cu, k_new=kn, v_new=vn, workspace=w)
+        o, lse = cuda_api.attn_chunk_paged(q, kp, vp, t, lens, cu, k_new=kn, v_new=vn, workspace=w)
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    assert cuda_api.device_status() == 0
