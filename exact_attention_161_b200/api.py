@@ -338,6 +338,9 @@ def _on(dev, stream, call):
     torch's current one, so that what the call allocates belongs to the stream it runs on."""
     if stream is None and dev == _current_device():
         return call(_raw_stream(dev))
+    where = getattr(stream, "device", None)
+    if where is not None and where.index != dev:
+        raise ValueError("the stream is on %s, the tensors are on cuda:%d" % (where, dev))
     with torch.cuda.device(dev):
         if stream is None:
             return call(_raw_stream(dev))

@@ -1,6 +1,7 @@
 """Attention over packed sequences, its gradients, chunks over the paged cache and rotary positions with
 several axes on the GPU, against the plain fp64 forms of packed_ref.py within their derived bounds."""
 import random
+import types
 
 import pytest
 import torch
@@ -862,4 +863,23 @@ def test_joined_parts_repeat_bit_for_bit(cuda_api, Hq, Hkv, D):
         cuda_api.attn_chunk_paged(other, kp, vp, t, lens, cu, k_new=kn, v_new=vn, workspace=w)
         o, lse = cuda_api.attn_chunk_paged(q, kp, vp, t, lens, cu, k_new=kn, v_new=vn, workspace=w)
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    assert cuda_api.device_status() == 0
+
+
+def test_a_stream_of_another_device_is_refused(cuda_api):
+    q, k, v, dout, _, cu = _batch([5], 4, 2, 64, 135)
+    kp, vp, table = _cache([5], 2, 64, 136)
+    lens = torch.tensor([5], dtype=torch.int32, device="cuda")
+    o, lse = cuda_api.attn_packed_fwd(q, k, v, cu)
+    pos = torch.zeros(1, 5, dtype=torch.int32, device="cuda")
+    here, there = torch.cuda.Stream(), q.get_device() + 1
+    calls = [lambda s: cuda_api.attn_packed_fwd(q, k, v, cu, stream=s),
+             lambda s: cuda_api.attn_packed_bwd(q, k, v, o, lse, dout, cu, stream=s),
+             lambda s: cuda_api.attn_chunk_paged(q, kp, vp, table.cuda(), lens, cu, k_new=k, v_new=v, stream=s),
+             lambda s: cuda_api.attn_rope_axes(q, k, pos, [32], stream=s)]
+    for call in calls:
+        with pytest.raises(ValueError, match="stream"):
+            call(types.SimpleNamespace(cuda_stream=here.cuda_stream, device=torch.device("cuda", there)))
+        call(types.SimpleNamespace(cuda_stream=here.cuda_stream, device=q.device))
+    torch.cuda.synchronize()
     assert cuda_api.device_status() == 0

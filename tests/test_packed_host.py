@@ -3,6 +3,7 @@ force, refusals before any CUDA call, and the gradients of the tests' plain form
 import ctypes
 import os
 import subprocess
+import types
 
 import pytest
 import torch
@@ -263,3 +264,10 @@ def test_plain_rotation_is_undone_by_its_inverse():
         y, _ = packed_ref.rope_axes(x, *a)
         z, _ = packed_ref.rope_axes(y, *a, inverse=True)
         assert (z - x).abs().max() < 1e-12 and (y - x).abs().max() > 0.1
+
+
+def test_a_stream_of_another_device_is_refused(api):
+    """Running there would hand one device's memory to another's kernels."""
+    other = types.SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream"):
+        api._on(0, other, lambda st: pytest.fail("called"))
