@@ -350,6 +350,11 @@ def _on(dev, stream, call):
             return call(stream.cuda_stream)
 
 
+def _window(window):
+    """The window as a C int (ctypes would pass the low 32 bits of a longer one; none that long cuts a key)."""
+    return max(-1, min(window, 2 ** 31 - 1))
+
+
 def _check_packed_shapes(q, k, v, cu_seqlens):
     if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or v.shape != k.shape:
         raise ValueError("q must be [T, Hq, D], k and v [T, Hkv, D]")
@@ -381,7 +386,7 @@ def attn_packed_fwd(q, k, v, cu_seqlens, causal=False, window=0, scale=0.0, o=No
         if ws is None:
             ws = q.new_empty(lib.attn_packed_fwd_workspace_size(T, S, Hq, Hkv, D), dtype=_U8)
         _check(lib.attn_packed_fwd(qp, kp, vp, qs, ks, vs, _ptr(cu_seqlens, "cu_seqlens", _I32, dev), S, T, Hq, Hkv, D,
-                                   bool(causal), window, scale, _ptr(out, "o", _BF16, dev),
+                                   bool(causal), _window(window), scale, _ptr(out, "o", _BF16, dev),
                                    None if stats is None else _ptr(stats, "lse", _F32, dev),
                                    _ptr(ws, "workspace", _U8, dev), ws.numel(), st))
         return out, stats
@@ -417,8 +422,8 @@ def attn_packed_bwd(q, k, v, o, lse, dout, cu_seqlens, causal=False, window=0, s
             ws = q.new_empty(lib.attn_packed_bwd_workspace_size(T, S, Hq, Hkv, D), dtype=_U8)
         _check(lib.attn_packed_bwd(qp, kp, vp, qs, ks, vs, _ptr(o, "o", _BF16, dev), _ptr(lse, "lse", _F32, dev),
                                    _ptr(dout, "dout", _BF16, dev), gqp, gkp, gvp, gqs, gks, gvs,
-                                   _ptr(cu_seqlens, "cu_seqlens", _I32, dev), S, T, Hq, Hkv, D, bool(causal), window,
-                                   scale, _ptr(ws, "workspace", _U8, dev), ws.numel(), st))
+                                   _ptr(cu_seqlens, "cu_seqlens", _I32, dev), S, T, Hq, Hkv, D, bool(causal),
+                                   _window(window), scale, _ptr(ws, "workspace", _U8, dev), ws.numel(), st))
         return gq, gk, gv
 
     return _on(dev, stream, call)
@@ -465,7 +470,7 @@ def attn_chunk_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, k_n
         _check(lib.attn_chunk_paged(qp, kp, vp, qs, ks, vs, _ptr(k_pages, "k_pages", _BF16, dev),
                                     _ptr(v_pages, "v_pages", _BF16, dev), _ptr(block_table, "block_table", _I32, dev),
                                     _ptr(seq_lens, "seq_lens", _I32, dev), _ptr(cu_seqlens, "cu_seqlens", _I32, dev), S,
-                                    T, max_blocks, num_pages, page_size, Hq, Hkv, D, window, scale,
+                                    T, max_blocks, num_pages, page_size, Hq, Hkv, D, _window(window), scale,
                                     _ptr(out, "o", _BF16, dev), None if stats is None else _ptr(stats, "lse", _F32, dev),
                                     _ptr(ws, "workspace", _U8, dev), ws.numel(), st))
         return out, stats
@@ -485,6 +490,8 @@ def attn_rope_axes(q, k, positions, sections, interleave_axes=False, per_axis_fr
     n_axes = len(sections)
     if positions.shape != (n_axes, T):
         raise ValueError("positions must be [len(sections), T]")
+    if any(abs(n) >= 2 ** 31 for n in sections):
+        raise ValueError("sections are 32-bit numbers")
     for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
         if t is not None and (like is None or t.shape != like.shape):
             raise ValueError("%s has another shape than its input" % name)

@@ -883,3 +883,19 @@ def test_a_stream_of_another_device_is_refused(cuda_api):
         call(types.SimpleNamespace(cuda_stream=here.cuda_stream, device=q.device))
     torch.cuda.synchronize()
     assert cuda_api.device_status() == 0
+
+
+def test_windows_past_32_bits(cuda_api):
+    q, k, v, dout, starts, cu = _batch([300, 20], 4, 2, 64, 137)
+    kp, vp, table = _cache([300, 20], 2, 64, 138)
+    lens = torch.tensor([300, 20], dtype=torch.int32, device="cuda")
+    run = lambda w: cuda_api.attn_packed_fwd(q, k, v, cu, causal=True, window=w) + \
+        cuda_api.attn_chunk_paged(q, kp, vp, table.cuda(), lens, cu, k_new=k, v_new=v, window=w)
+    o, lse = cuda_api.attn_packed_fwd(q, k, v, cu, causal=True)
+    ref = packed_ref.packed(q, k, v, starts, True, 0, dout=dout)
+    want = run(0)
+    for w in (2 ** 32 + 5, -2 ** 32 + 5, 2 ** 31):
+        assert all(torch.equal(x, y) for x, y in zip(run(w), want))
+        for name, x in zip(("dq", "dk", "dv"), cuda_api.attn_packed_bwd(q, k, v, o, lse, dout, cu, causal=True, window=w)):
+            packed_ref.check(name, x, ref)
+    assert cuda_api.device_status() == 0

@@ -271,3 +271,15 @@ def test_a_stream_of_another_device_is_refused(api):
     other = types.SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="stream"):
         api._on(0, other, lambda st: pytest.fail("called"))
+
+
+def test_numbers_past_32_bits_are_not_cut_off(api):
+    """The C entry points take 32-bit integers, of which ctypes would pass the low bits: a window that long cuts
+    nothing, a section that long is refused."""
+    for window, passed in ((5, 5), (0, 0), (-3, -1), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                           (2 ** 32 + 5, 2 ** 31 - 1), (-2 ** 32 + 5, -1)):
+        assert ctypes.c_int(api._window(window)).value == passed
+    q = torch.zeros(4, 8, 128, dtype=torch.bfloat16)
+    for sections in ([2 ** 32 + 64], [-2 ** 32 + 64]):
+        with pytest.raises(ValueError, match="sections"):
+            api.attn_rope_axes(q, None, torch.zeros(1, 4, dtype=torch.int32), sections)
