@@ -899,3 +899,122 @@ def test_windows_past_32_bits(cuda_api):
         for name, x in zip(("dq", "dk", "dv"), cuda_api.attn_packed_bwd(q, k, v, o, lse, dout, cu, causal=True, window=w)):
             packed_ref.check(name, x, ref)
     assert cuda_api.device_status() == 0
+
+
+def _expected_list(new, keys, TT, Hkv, causal, window, starts, paged):
+    """The rule of the forward's work list, restated: the blocks (first row, position, sequence or first key row,
+    keys, first tile, tiles, tokens), their costs, the limit, and whether the list is cut."""
+    blocks = []
+    for s, (n, m) in enumerate(zip(new, keys)):
+        for first in range(0, n, 2 * TT):
+            tok = min(2 * TT, n - first)
+            pos = m - n + first
+            lo = max(0, pos - window + 1) if window > 0 else 0
+            hi = pos + tok if causal else m
+            jb = lo // 128
+            tiles = (hi + 127) // 128 - jb
+            blocks.append((starts[s] + first, pos, s if paged else starts[s], m, jb, tiles, tok))
+    cost = lambda tiles, tok: (5 * tiles + 7) // 8 if tok <= TT else tiles
+    costs = [cost(b[5], b[6]) for b in blocks]
+    limit, longest = max(4, -(-sum(costs) * Hkv // 296)), max(costs)
+
+    def load(cut):
+        """The sum of every 148th item of the descending list, in steps of the counting sort's buckets."""
+        hist = [0] * 1024
+        for b, c in zip(blocks, costs):
+            parts = -(-c // limit) if cut and c > limit else 1
+            for i in range(parts):
+                t = b[5] // parts + (i < b[5] % parts)
+                hist[1023 - cost(t, b[6]) * 1023 // longest] += 1
+        at = total = 0
+        for i, n in enumerate(hist):
+            if n:
+                total += (-(-(at + n) * Hkv // 148) - -(-at * Hkv // 148)) * -(-(1023 - i) * longest // 1023)
+            at += n
+        return total
+
+    join = 6 if any(c > limit and 4 * b[6] > TT for b, c in zip(blocks, costs)) else 2
+    return blocks, costs, cost, limit, longest, longest > limit and load(True) + join < load(False)
+
+
+def _check_list(ws, S, expected):
+    blocks, costs, cost, limit, longest, cut = expected
+    want = set()
+    for b, c in zip(blocks, costs):
+        parts = -(-c // limit) if cut and c > limit else 1
+        at = b[4]
+        for i in range(parts):
+            t = b[5] // parts + (i < b[5] % parts)
+            want.add(b[:4] + (at, t, b[6] | i << 10 | (parts - 1) << 20))
+            at += t
+    items = _plan_items(ws, S).tolist()
+    assert len(items) == len(want) and {tuple(x[:7]) for x in items} == want
+    order = [cost(x[5], x[6] & 1023) * 1023 // longest for x in items]
+    assert order == sorted(order, reverse=True)
+    taken = [r for slot, p in {(x[7], (x[6] >> 20) + 1) for x in items if x[6] >> 20} for r in range(slot, slot + p)]
+    assert sorted(taken) == list(range(len(taken)))  # every slot is one part's
+    return cut
+
+
+def test_work_list_is_the_rule_s(cuda_api):
+    """The list that the device builds: every block's tiles once, longest first, cut where the rule says so."""
+    rng = random.Random(140)
+    cuts = []
+    for Hq, Hkv, causal, window in ((8, 2, True, 0), (4, 4, False, 0), (6, 2, True, 300), (8, 1, True, 0), (64, 1, True, 0)):
+        for lens in ([1500], [2500, 1, 3000], [rng.randint(0, 400) for _ in range(40)], [1] * 5,
+                     [rng.choice([0, 1, 2, 150]) for _ in range(2300)]):
+            q, k, v, _, starts, cu = _batch(lens, Hq, Hkv, 64, 141)
+            w = torch.empty(cuda_api.packed_fwd_workspace_size(sum(lens), len(lens), Hq, Hkv, 64), dtype=torch.uint8,
+                            device="cuda")
+            cuda_api.attn_packed_fwd(q, k, v, cu, causal=causal, window=window, workspace=w)
+            cuts.append(_check_list(w, len(lens), _expected_list(lens, lens, 128 // (Hq // Hkv), Hkv, causal, window,
+                                                                 starts, False)))
+        for new, ctx in (([1] * 8, [4000] * 8), ([1, 300, 1, 0, 20], [9000, 2000, 3, 77, 500]), ([1], [2000]),
+                         ([1] * 200, [rng.randint(0, 900) for _ in range(200)])):
+            if not causal:
+                continue
+            total = [c + n for c, n in zip(ctx, new)]
+            kp, vp, table = _cache(total, Hkv, 64, 142)
+            q, kn, vn, _, starts, cu = _batch(new, Hq, Hkv, 64, 143)
+            w = torch.empty(cuda_api.chunk_workspace_size(sum(new), len(new), table.shape[1], 16, Hq, Hkv, 64),
+                            dtype=torch.uint8, device="cuda")
+            cuda_api.attn_chunk_paged(q, kp, vp, table.cuda(), torch.tensor(total, dtype=torch.int32, device="cuda"),
+                                      cu, k_new=kn, v_new=vn, window=window, workspace=w)
+            cuts.append(_check_list(w, len(new), _expected_list(new, total, 128 // (Hq // Hkv), Hkv, True, window,
+                                                                starts, True)))
+    assert any(cuts) and not all(cuts)
+    assert cuda_api.device_status() == 0
+
+
+def test_backward_tile_list(cuda_api):
+    """The backward's list: every 128 keys of every sequence once, a sequence's tiles in their order, sequences
+    from the longest to the shortest (to the 1,023rd part of the longest), query tiles numbered through."""
+    rng = random.Random(144)
+    for Hq, Hkv in ((8, 2), (6, 2), (4, 4)):
+        TT = 128 // (Hq // Hkv)
+        for lens in ([700], [1, 0, 300, 128, 129, 0, 2000, 5], [rng.choice([0, 1, 2, 150, 300]) for _ in range(2300)]):
+            S, T = len(lens), sum(lens)
+            q, k, v, dout, starts, cu = _batch(lens, Hq, Hkv, 64, 145)
+            w = torch.empty(cuda_api.packed_bwd_workspace_size(T, S, Hq, Hkv, 64), dtype=torch.uint8, device="cuda")
+            o, lse = cuda_api.attn_packed_fwd(q, k, v, cu, causal=True)
+            cuda_api.attn_packed_bwd(q, k, v, o, lse, dout, cu, causal=True, workspace=w)
+            up = lambda x: (x + 255) // 256 * 256
+            at = 256 + up((S + 1) * 4) + 2 * up(S * 4)
+            n_max = T // 128 + min(S, T)
+            want, base = [], 0
+            for s, n in enumerate(lens):
+                want += [[starts[s], n, t, base] for t in range((n + 127) // 128)]
+                base += -(-n // TT)
+            n = int(w[:4].cpu().view(torch.int32))
+            tiles = w[at:at + 16 * n].cpu().clone().view(torch.int32).view(n, 4).tolist()
+            assert tiles == want
+            at += up(16 * n_max)
+            order = w[at:at + 4 * n].cpu().clone().view(torch.int32).tolist()
+            assert sorted(order) == list(range(n))
+            most = max((x + 127) // 128 for x in lens)
+            left = [((x[1] + 127) // 128 * 1023 // most, x[0], x[2]) for x in (want[i] for i in order)]
+            heads = [x for x in left if x[2] == 0]
+            assert [x[0] for x in heads] == sorted((x[0] for x in heads), reverse=True)
+            for a, b in zip(left, left[1:]):
+                assert b[2] == 0 or (b[1] == a[1] and b[2] == a[2] + 1)
+    assert cuda_api.device_status() == 0

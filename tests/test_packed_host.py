@@ -283,3 +283,80 @@ def test_numbers_past_32_bits_are_not_cut_off(api):
     for sections in ([2 ** 32 + 64], [-2 ** 32 + 64]):
         with pytest.raises(ValueError, match="sections"):
             api.attn_rope_axes(q, None, torch.zeros(1, 4, dtype=torch.int32), sections)
+
+
+@pytest.fixture(scope="module")
+def costs(tmp_path_factory):
+    """What the work list is cut by, compiled for the host."""
+    d = tmp_path_factory.mktemp("costs")
+    src = d / "costs.cpp"
+    src.write_text('#include "plan.cuh"\nusing namespace attn;\nextern "C" {\n'
+                   'void keys(int f, int l, int m, int c, int w, int* o) { KeyTiles t = key_tiles(f, l, m, c, w);'
+                   ' o[0] = t.jb; o[1] = t.n; }\n'
+                   'int cost(int t, int one) { return plan_cost(t, one); }\n'
+                   'int limit(long long t, int h) { return plan_limit(t, h); }\n'
+                   'int parts(int t, int l) { return plan_parts(t, l); }\n'
+                   'void part(int t, int p, int i, int* o) { plan_part(t, p, i, o[0], o[1]); }\n'
+                   'void sizes(long long T, long long S, int TT, long long m, int h, long long* o)'
+                   ' { PlanLayout L = plan_layout(T, S, TT, m, h, 128); o[0] = L.max_slots; o[1] = L.max_items; }\n}\n')
+    lib = d / "libcosts.so"
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I",
+                    os.path.join(ROOT, "exact_attention_161_b200", "csrc"), str(src), "-o", str(lib)], check=True)
+    p = ctypes.CDLL(str(lib))
+    p.limit.argtypes = [ctypes.c_longlong, ctypes.c_int]
+    p.sizes.argtypes = [ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong, ctypes.c_int,
+                        ctypes.POINTER(ctypes.c_longlong)]
+    return p
+
+
+@pytest.mark.parametrize("Hkv", [1, 2, 8, 32])
+@pytest.mark.parametrize("TT", [1, 16, 32, 42, 128])
+@pytest.mark.parametrize("causal,window", [(1, 0), (0, 0), (1, 1), (1, 700)])
+def test_list_cut_by_cost_fits_the_workspace(costs, TT, Hkv, causal, window):
+    """The device's rule: blocks are cut by what they cost (5/8 of its tiles for a block of at most TT tokens), in
+    calls of single tokens, of short chunks among full blocks, and of whole prompts. Items and slots stay within
+    what the layout reserves, no part is empty, and the parts cover the block's tiles once."""
+    g = torch.Generator().manual_seed(TT * 1000 + Hkv * 10 + causal + window)
+    draw = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    cut_one = 0
+    for trial in range(20):
+        S = draw(1, 70)
+        top = int(10 ** (torch.rand(1, generator=g).item() * 4.5)) + 1
+        kind = trial % 4
+        ctx = [draw(0, top) for _ in range(S)]
+        if kind == 0:  # a token each
+            new = [1] * S
+        elif kind == 1:  # short chunks
+            new = [draw(0, 2 * TT) for _ in range(S)]
+        elif kind == 2:  # single tokens beside chunks
+            new = [1 if draw(0, 3) else draw(1, 3000) for _ in range(S)]
+        else:  # packed prompts
+            new, ctx = [draw(0, top) for _ in range(S)], [0] * S
+        T = sum(new)
+        if T == 0:
+            continue
+        max_keys = T if kind == 3 else (max(c + n for c, n in zip(ctx, new)) + 15) // 16 * 16
+        blocks = []
+        for c, n in zip(ctx, new):
+            for first in range(0, n, 2 * TT):
+                last = min(n, first + 2 * TT) - 1
+                tiles = _pair(costs.keys, c + first, c + last, c + n, causal, window)[1]
+                one = int(last - first + 1 <= TT)
+                cost = costs.cost(tiles, one)
+                assert 1 <= cost <= tiles and cost >= tiles / 2
+                blocks.append((tiles, cost, one))
+        limit = costs.limit(sum(x[1] for x in blocks), Hkv)
+        slots = items = 0
+        for tiles, cost, one in blocks:
+            p = costs.parts(cost, limit)
+            assert 1 <= p <= 1023 and (p == 1) == (cost <= limit)
+            edges = [_pair(costs.part, tiles, p, i) for i in range(p)]
+            assert edges[0][0] == 0 and edges[-1][1] == tiles and all(a[1] == b[0] for a, b in zip(edges, edges[1:]))
+            assert all(b > a for a, b in edges)
+            items += p
+            slots += p if p > 1 else 0
+            cut_one += p > 1 and one
+        room = (ctypes.c_longlong * 2)()
+        costs.sizes(T, S, TT, max_keys, Hkv, room)
+        assert slots <= room[0] and items <= room[1]
+    assert cut_one > 0 or window in (1, 700)
