@@ -7,9 +7,11 @@
 // ("attention-transformers", Q "How does Rotary Position Embedding (RoPE) work?").
 //
 // Positions are device data of any int32 value, so there is no table: the angle is formed in
-// revolutions in fp64 (pos * theta / 2 pi: positions far out lose nothing; at |pos| = 2^31 the
-// fraction is right to 4e-8 revolutions), reduced to a fraction in [-1/2, 1/2] and handed to
-// sincospif in fp32. The products and the sum are fp32; one rounding to bf16 at the store.
+// revolutions in fp64 (pos / pos_scale * theta / 2 pi), reduced to a fraction in [-1/2, 1/2] and handed to
+// sincospif in fp32. The constant, the quotient and the product are each off by at most 2^-53 of the
+// revolutions, the fraction in fp32 by 2^-26: 1.2e-7 revolutions together at |pos| = 2^31, pos_scale = 1 and
+// theta = 1; at smaller theta the power adds its own rounding to fewer revolutions, and a pos_scale below 1
+// makes them and the error so many times larger. The products and the sum are fp32; one rounding to bf16 at the store.
 //
 // Bound: HBM (each element is read and written once). A warp rotates one token's heads (or a share of
 // them, where there are few tokens): each lane computes the angles of one or two pairs, once per token and

@@ -147,7 +147,8 @@ size_t attn_bwd_workspace_size(int B, int Hq, int Hkv, int N, int D, float rope_
  * with q, k rotated; the gradients of the unrotated inputs are rotated back. For GQA, dk and dv of a
  * K/V head sum over its query heads. dk and dv are accumulated in a fixed order and repeat bit for
  * bit; dq is a sum of fp32 partials (one per 128-key tile) added in device memory in the order the
- * tiles finish, so two calls may differ by one bf16 unit in the last place.
+ * tiles finish: two calls may differ by (tiles - 1) 2^-23 times the sum of the partials' magnitudes,
+ * times the scale, before the rounding to bf16 (where partials cancel, by more than a unit of the result).
  *
  *   q, k, v, causal, window, rope_base, scale, B, Hq, Hkv, N, D   as given to attn_fwd
  *   o      bf16 [B, Hq, N, D] and lse fp32 [B, Hq, N]: attn_fwd's outputs for these inputs
@@ -296,6 +297,8 @@ attn_status attn_decode_paged_noalloc(const void* q, const void* k_pages, const 
  *   *_stride     elements from one token's row to the next (multiple of 8, >= heads * D): q, k and v
  *          may be views of one projection's output. A token's heads are contiguous, 16-byte aligned.
  *   T = 0        is valid: nothing is done.
+ *   Outputs must not overlap inputs or one another (o over q, dk over k), but for attn_rope_axes in place;
+ *          views of one tensor that share no element, as of a fused gradient, are fine.
  *   workspace    device scratch of the size the *_workspace_size function gives for the call's sizes,
  *          16-byte aligned, owned by the caller, any initial contents, overwritten; calls that overlap
  *          on the GPU, and captured graphs that may run side by side, need their own.
@@ -344,8 +347,8 @@ size_t attn_packed_bwd_workspace_size(int T, int num_seqs, int Hq, int Hkv, int 
  *   dout   bf16 [T, Hq, D] contiguous: gradient of the loss with respect to o, finite within sequences
  *   dq     bf16 [T, Hq, D]; dk, dv bf16 [T, Hkv, D]: written, with strides of their own
  * dk and dv repeat bit for bit; dq is a sum of fp32 partials (one per 128-key tile) added in the order
- * the tiles finish, so for sequences of more than 256 tokens two calls may differ by one bf16 unit in
- * the last place (a sum of at most two partials onto zero has one rounding whatever the order).
+ * the tiles finish, so for sequences of more than 256 tokens two calls may differ as attn_bwd's do (a sum
+ * of at most two partials onto zero has one rounding whatever the order).
  */
 attn_status attn_packed_bwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                             int64_t v_stride, const void* o, const float* lse, const void* dout, void* dq, void* dk,
@@ -381,6 +384,8 @@ size_t attn_chunk_workspace_size(int T, int num_seqs, int max_blocks_per_seq, in
  * Bad offsets: no output is written; tokens of sequences whose own two offsets are valid may be appended.
  * With window > 0, pages that lie wholly before the window of the sequence's first new token are not
  * read: their block-table entries may hold anything (a page that was given back, -1).
+ * Without a window, where every sequence brings one token that the cache already holds, attn_decode_paged does the same
+ * and is faster (64 sequences on 4,000 tokens each 176 us against 201, on 16,000 612 against 727).
  */
 attn_status attn_chunk_paged(const void* q, const void* k_new, const void* v_new, int64_t q_stride, int64_t k_stride,
                              int64_t v_stride, void* k_pages, void* v_pages, const int32_t* block_table,
