@@ -48,7 +48,7 @@
 //   Short sequences: 4,200 to 5,500 clocks an item outside its steps (the last tile's masks, the last
 //     product, O to memory, the first scores): 24 prompts of 100 to 1,500 tokens 137 to 141 us, of which O's stores
 //     cost 8 and the masks 4 (left out in copies).
-//   D = 64: the exponentials (SFU 60% busy); 12 images of 200 to 3,300 patches 200 us, 590 TFLOP/s.
+//   D = 64: the exponentials (SFU 67% busy); 12 images of 200 to 3,300 patches 200 us, 590 TFLOP/s.
 //   Single tokens: reading the keys, 64 on 16,000 tokens each 5.8 TB/s (0.89 of the copy rate).
 // Registers: 168 a thread, all that 12 warps leave each other; 20 to 40 bytes a thread are spilled.
 #pragma once
