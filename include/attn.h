@@ -303,7 +303,8 @@ attn_status attn_decode_paged_noalloc(const void* q, const void* k_pages, const 
  *          16-byte aligned, owned by the caller, any initial contents, overwritten; calls that overlap
  *          on the GPU, and captured graphs that may run side by side, need their own.
  * Within a sequence K and V must be finite. A query row that is not spoils itself only: where a visible
- * score is NaN or +inf, its o and lse are NaN; where all are -inf, o is NaN and lse -inf. Values are bf16; scores, softmax statistics and sums are
+ * score is NaN or +inf, its o and lse are NaN; where all are -inf, o is NaN and lse -inf. In the backward it
+ * spoils its own dq, and dk and dv of its sequence (a product's zero times NaN), but no other sequence. Values are bf16; scores, softmax statistics and sums are
  * fp32, P is rounded to bf16 for its product as in attn_fwd. Constraints: D in {64, 128},
  * Hq / Hkv <= 128 (else ATTN_ERR_UNSUPPORTED), 128 * Hkv * (T / floor(128 * Hkv / Hq) + num_seqs) < 2^31
  * (about T * Hq). Nothing is allocated or

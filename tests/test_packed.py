@@ -1018,3 +1018,23 @@ def test_backward_tile_list(cuda_api):
             for a, b in zip(left, left[1:]):
                 assert b[2] == 0 or (b[1] == a[1] and b[2] == a[2] + 1)
     assert cuda_api.device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_backward_of_a_query_that_is_not_finite(cuda_api, D):
+    """One NaN and one infinite query among finite ones: their own dq is NaN, every other row's dq is right (it
+    takes part in no other row's sum), and so are the gradients of the other sequences."""
+    q, k, v, dout, starts, cu = _batch([150, 600, 90], 8, 2, D, 146)
+    q[200, 0, 3], q[500, 5, 7] = NAN, float("inf")
+    o, lse = cuda_api.attn_packed_fwd(q, k, v, cu, causal=True)
+    grads = cuda_api.attn_packed_bwd(q, k, v, o, lse, dout, cu, causal=True)
+    ref = packed_ref.packed(q, k, v, starts, True, 0, dout=dout)
+    bad = torch.zeros(q.shape[0], 8, dtype=torch.bool, device="cuda")
+    bad[200, 0] = bad[500, 5] = True
+    assert bool(torch.isnan(grads[0][bad].float()).all())
+    ref["dq"][bad] = NAN  # (compared above)
+    packed_ref.check("dq", grads[0], ref)
+    for name, x in zip(("dk", "dv"), grads[1:]):
+        for a, b in ((0, 150), (750, 840)):
+            packed_ref.check(name, x[a:b], {n: y[a:b] for n, y in ref.items() if n.startswith(name)})
+    assert cuda_api.device_status() == 0
